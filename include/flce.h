@@ -304,6 +304,121 @@ flce_status_t flce_pairwise_logistic(const float* d_row_loss, const int32_t* y, 
                                      double* d_loss, double* d_logp, double* d_grad_logp, float* d_row_weight,
                                      int32_t* d_status, cudaStream_t stream);
 
+/* ---- Post-training losses of the output layer -----------------------------
+ * Further losses of the family that the paragraph above names, each with its
+ * gradient: a clipped policy loss with a KL term, on per-row losses
+ * (flce_clipped_policy), on given logits (flce_policy_loss) and through the
+ * head without its logits (flce_policy_forward_backward); and distillation
+ * from a teacher's largest logits, on given logits (flce_distill_topk) and
+ * through the head (flce_distill_forward_backward).  The pages name the
+ * family, not these formulas.
+ *
+ * Rows whose target is ignore_index take part in nothing: whatever their
+ * logits, log-probabilities, advantages or teacher entries hold (NaN
+ * included), their outputs are 0.  Reductions are those of
+ * flce_forward_backward_ex: the loss is sum_i s_i L_i over the other rows with
+ * s_i = 1/n, 1 or grad_row_scale[i].  A mean over each answer's tokens and
+ * then over the answers is NONE with s_i = 1 / (answers * tokens of i's answer).
+ *
+ * Logit tensors of these entries may be bf16, fp16 or fp32 (flce_dtype_t),
+ * rows `ld` elements apart (ld >= V), elements of a row adjacent; pointers
+ * need the element's alignment only.  dlogits has the logits' type and its
+ * own row stride; it may be the logits (same pointer and stride: in place), is
+ * NULL for a forward-only call, and otherwise must not overlap the logits'
+ * memory range.  Columns beyond V are neither read nor written. */
+typedef enum { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_FP16 = 1, FLCE_DTYPE_FP32 = 2 } flce_dtype_t;
+
+/* Clipped policy loss with a KL term on per-row log-probabilities lp_i = -l_i
+ * (row losses of flce_forward_backward_ex or flce_cross_entropy):
+ *   r_i  = exp(lp_i - old_i)                     (d_old_logp NULL: r_i = 1)
+ *   kl_i = exp(ref_i - lp_i) - (ref_i - lp_i) - 1  (d_ref_logp NULL: 0)
+ *   L_i  = -min(r_i A_i, clip(r_i, 1 - clip_low, 1 + clip_high) A_i) + kl_coef kl_i
+ *   row_weight[i] = s_i dL_i / dl_i: the upstream gradient of l_i, to pass as
+ *                   grad_row_scale with reduction NONE
+ * A ratio on a clip border counts as not clipped (its gradient passes).
+ * clip_low in [0, 1], clip_high >= 0 (infinity: no upper border); kl_coef
+ * finite, and 0 when d_ref_logp is NULL.  All pointers DEVICE: fp32 [N] inputs
+ * and outputs, y int32 [N], d_loss fp64 [1], d_status int32 [1]; workspace of
+ * flce_ce_workspace_size(N, 1) bytes, 256-byte aligned.  Asynchronous; the
+ * sums are fp64 in a fixed order. */
+flce_status_t flce_clipped_policy(const float* d_row_loss, const int32_t* y, int64_t N, int32_t ignore_index,
+                                  const float* d_old_logp, const float* d_advantage, const float* d_ref_logp,
+                                  double clip_low, double clip_high, double kl_coef, int32_t reduction,
+                                  const float* d_row_scale, double* d_loss, float* d_policy_loss, float* d_kl,
+                                  float* d_row_weight, int32_t* d_status, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/* The same loss on given logits z, with an entropy term.  With x = z / temperature,
+ *   lp_i = x_{i,y_i} - lse(x_i),  H_i = -sum_j p_ij log p_ij,
+ *   L_i as above - entropy_coef H_i;
+ * dlogits = d loss / d z (temperature's 1/T included).  d_logp, d_entropy and
+ * d_kl (DEVICE fp32 [N]) receive lp, H and kl, 0 on ignored rows.  A logit of
+ * -infinity is a vocabulary entry of probability 0.  Targets outside [0, V) set
+ * FLCE_ERR_TARGET_OUT_OF_RANGE in d_status and count as ignored in the sums.
+ * workspace: flce_ce_workspace_size(N, V) bytes.  Asynchronous; may be
+ * captured in a CUDA graph. */
+flce_status_t flce_policy_loss(const void* logits, int32_t dtype, int64_t ld, const int32_t* y, int64_t N, int64_t V,
+                               int32_t ignore_index, double temperature, const float* d_old_logp,
+                               const float* d_advantage, const float* d_ref_logp, double clip_low, double clip_high,
+                               double kl_coef, double entropy_coef, int32_t reduction, const float* grad_row_scale,
+                               float* d_loss, float* d_logp, float* d_entropy, float* d_kl, int32_t* d_status,
+                               void* dlogits, int64_t ld_dlogits, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/* Distillation from a teacher's K largest logits per row (1 <= K <= 1024):
+ *   q_i  = softmax over the row's entries of teacher_logits / temperature, or
+ *          exp(teacher_logits / temperature - teacher_lse) when d_teacher_lse is
+ *          given (the teacher's own log-sum-exp over its whole vocabulary, at
+ *          the same temperature; the mass outside the K entries is dropped),
+ *   p_i  = softmax(z_i / temperature),
+ *   L_i  = kd_weight sum_k q_ik (log q_ik - log p_{i,id_ik})
+ *        + ce_weight (lse(z_i) - z_{i,y_i})          (hard labels at temperature 1)
+ * d_teacher_ids int32 [N][K] in any order, teacher_logits [N][K] of
+ * teacher_dtype, both contiguous; a negative id is an empty slot, an id >= V
+ * sets FLCE_ERR_TARGET_OUT_OF_RANGE and counts as empty, an id that appears
+ * twice counts with both its entries, and a row with no entry has L_i's second
+ * term alone.  Terms with q = 0 are 0.  No T^2 factor is applied: put it into
+ * kd_weight.  d_row_loss (fp32 [N] or NULL) receives L_i.  Other arguments as
+ * flce_policy_loss. */
+flce_status_t flce_distill_topk(const void* logits, int32_t dtype, int64_t ld, const int32_t* y, int64_t N, int64_t V,
+                                int32_t ignore_index, const int32_t* d_teacher_ids, const void* d_teacher_logits,
+                                int32_t teacher_dtype, int32_t K, const float* d_teacher_lse, double temperature,
+                                double kd_weight, double ce_weight, int32_t reduction, const float* grad_row_scale,
+                                float* d_loss, float* d_row_loss, int32_t* d_status, void* dlogits,
+                                int64_t ld_dlogits, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* The clipped policy loss through the head: pass 1 gives the rows'
+ * log-probabilities of z = X W^T, the combine step turns them into the loss and
+ * each row's weight, and pass 2 forms dX and dW: the two passes of a
+ * cross-entropy call, where separate calls (row losses, flce_clipped_policy,
+ * gradients) run pass 1 twice.  d_logp (fp32 [N]) receives lp_i, 0 on ignored
+ * rows.  Other arguments and results as flce_forward_backward_ex (dX and dW
+ * both NULL: loss and log-probabilities only) and flce_clipped_policy. */
+flce_status_t flce_policy_forward_backward(const uint16_t* X, const uint16_t* W, const int32_t* y, int64_t N,
+                                           int64_t H, int64_t V, int32_t ignore_index, const float* d_old_logp,
+                                           const float* d_advantage, const float* d_ref_logp, double clip_low,
+                                           double clip_high, double kl_coef, int32_t reduction,
+                                           const float* grad_row_scale, const int32_t* d_mean_count, float* d_loss,
+                                           float* d_logp, int32_t* d_status, uint16_t* dX, uint16_t* dW,
+                                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Distillation through the head, z = X W^T never stored.  Loss and teacher
+ * arguments as flce_distill_topk, except that ce_weight needs temperature 1
+ * (FLCE_ERR_UNSUPPORTED otherwise: a logit tile is turned into one softmax);
+ * other arguments as flce_forward_backward_ex.  workspace:
+ * flce_distill_workspace_size(N, H, K, 0) bytes, or with `reorder` != 0 the
+ * size that lets the call reorder token rows; both independent of V, 0 for
+ * invalid sizes. */
+size_t flce_distill_workspace_size(int64_t N, int64_t H, int32_t K, int32_t reorder);
+flce_status_t flce_distill_forward_backward(const uint16_t* X, const uint16_t* W, const int32_t* y, int64_t N,
+                                            int64_t H, int64_t V, int32_t ignore_index, const int32_t* d_teacher_ids,
+                                            const void* d_teacher_logits, int32_t teacher_dtype, int32_t K,
+                                            const float* d_teacher_lse, double temperature, double kd_weight,
+                                            double ce_weight, int32_t reduction, const float* grad_row_scale,
+                                            const int32_t* d_mean_count, float* d_loss, float* d_row_loss,
+                                            int32_t* d_status, uint16_t* dX, uint16_t* dW, void* workspace,
+                                            size_t workspace_bytes, cudaStream_t stream);
+
 /* Allocation-free variant of flce_forward_backward, for callers that cannot
  * allocate device memory: a plug-in or custom operator that is handed only the
  * tensors it works on and has no allocator to ask for scratch, and processes
@@ -401,7 +516,9 @@ flce_status_t flce_profile_read(int32_t* launches, double* total_ms);
  * (flce_forward_backward_host), its copies: kind 8 host to device (X and y
  * on the caller's stream, each W piece on the copy stream), kind 9 device to
  * host (each section's dW rows on the copy stream, then dX and the loss on
- * the caller's stream); flce_kernel_name names them too.  Waits for the
+ * the caller's stream), and the launches of the post-training losses (kind 10
+ * losses on given logits, 11 the clipped policy rows, 12 a distillation call's
+ * teacher lists); flce_kernel_name names them too.  Waits for the
  * recorded events and writes, for the first `capacity` intervals, kinds[i]
  * and their begin and end in milliseconds after the begin of the first
  * interval (HOST arrays of `capacity` entries); *count receives the number

@@ -28,3 +28,11 @@ from .flce import (  # noqa: F401
     workspace_size,
     workspace_size_reorder,
 )
+from .post_training import (  # noqa: F401
+    clipped_policy,
+    distill_forward_backward,
+    distill_topk,
+    distill_workspace_size,
+    policy_forward_backward,
+    policy_loss,
+)

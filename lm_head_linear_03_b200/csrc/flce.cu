@@ -13,6 +13,7 @@
 
 #include "flce.h"
 #include "flce_kernels.cuh"
+#include "logit_losses.cuh"
 
 namespace {
 
@@ -114,6 +115,31 @@ CeLayout ce_ws_layout(int64_t N) {
   return L;
 }
 
+// Area behind the head's workspace for a distillation call: each row's sorted
+// list of vocabulary entries and its constants.
+struct ListLayout {
+  size_t ids, c, z, count, dense, kconst, klse, kdot, total;
+};
+ListLayout list_layout(int64_t N, int64_t K, size_t off) {
+  ListLayout L{};
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  const size_t n = static_cast<size_t>(N), e = n * (static_cast<size_t>(K) + 1);
+  L.ids = take(e * 4);
+  L.c = take(e * 4);
+  L.z = take(e * 4);
+  L.count = take(n * 4);
+  L.dense = take(n * 4);
+  L.kconst = take(n * 8);
+  L.klse = take(n * 8);
+  L.kdot = take(n * 8);
+  L.total = off;
+  return L;
+}
+
 // ------------------------------------------------------------ device info --
 struct DevInfo {
   bool ok = false;
@@ -150,12 +176,12 @@ cudaError_t set_kernel_attrs(int dev) {
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_attr_set[dev]) return cudaSuccess;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(flce_pass1_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P1_SMEM_BYTES)) !=
-      cudaSuccess)
-    return e;
-  if ((e = cudaFuncSetAttribute(flce_pass2_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) !=
-      cudaSuccess)
-    return e;
+  for (auto k : {flce_pass1_kernel<false>, flce_pass1_kernel<true>})
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P1_SMEM_BYTES)) != cudaSuccess)
+      return e;
+  for (auto k : {flce_pass2_kernel<false>, flce_pass2_kernel<true>})
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES)) != cudaSuccess)
+      return e;
   // How many SM pairs the GEMM kernels can occupy at once (persistent grids).
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * 1024, 1, 1);
@@ -168,12 +194,19 @@ cudaError_t set_kernel_attrs(int dev) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  int clusters = 0, clusters2 = 0;
+  int clusters = INT_MAX;
   cfg.dynamicSmemBytes = P1_SMEM_BYTES;
-  if ((e = cudaOccupancyMaxActiveClusters(&clusters, flce_pass1_kernel, &cfg)) != cudaSuccess) return e;
+  for (auto k : {flce_pass1_kernel<false>, flce_pass1_kernel<true>}) {
+    int c = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&c, k, &cfg)) != cudaSuccess) return e;
+    clusters = std::min(clusters, c);
+  }
   cfg.dynamicSmemBytes = SMEM_BYTES;
-  if ((e = cudaOccupancyMaxActiveClusters(&clusters2, flce_pass2_kernel, &cfg)) != cudaSuccess) return e;
-  clusters = std::min(clusters, clusters2);
+  for (auto k : {flce_pass2_kernel<false>, flce_pass2_kernel<true>}) {
+    int c = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&c, k, &cfg)) != cudaSuccess) return e;
+    clusters = std::min(clusters, c);
+  }
   if (clusters <= 0) return cudaErrorInvalidConfiguration;
   g_dev[dev].max_clusters = clusters;
   g_attr_set[dev] = true;
@@ -359,6 +392,15 @@ cudaError_t pipe_resources(PipeRes** out) {
   return cudaSuccess;
 }
 
+// A distillation call's teacher (see flce_distill_forward_backward).
+struct TeacherIn {
+  const int32_t* ids;
+  const void* logits;
+  int dtype, K;
+  const float* lse;
+  double temperature, kd, ce;
+};
+
 struct Options {
   int reduction = RED_MEAN;
   const float* grad_row_scale = nullptr;
@@ -375,6 +417,9 @@ struct Options {
   int shards = 0;
   const float* all_lse = nullptr;
   const float* all_zy = nullptr;
+  const PolicyArgs* policy = nullptr;  // policy loss of the rows' log-probabilities, which go to `logp`
+  float* logp = nullptr;
+  const TeacherIn* teacher = nullptr;  // distillation; its lists lie behind the head's own workspace
   const PipeCtx* pipe = nullptr;  // host-buffer call: pieces of pass 1, sections of pass 2
   // failure probe only: a shorter wait limit, and dW mainloops that wait for
   // one G tile more than the queue produces
@@ -395,7 +440,9 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
   if (device_info(&di, &dev) != cudaSuccess) return cuda_fail(__LINE__);  // now with max_clusters
   // reordered rows need the packed-X area: only a large enough workspace has it
   // (vocabulary shards keep the caller's order: their statistics are per row)
-  const WsLayout L = ws_layout(N, H, opt.combine == COMBINE_FULL && ws_bytes >= ws_layout(N, H, true).total);
+  const size_t list_bytes = opt.teacher ? list_layout(N, opt.teacher->K, 0).total : 0;
+  const WsLayout L =
+      ws_layout(N, H, opt.combine == COMBINE_FULL && ws_bytes >= ws_layout(N, H, true).total + list_bytes);
   const Plan P = make_plan(N, H, V, di.max_clusters);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(ws + L.ctrl);
@@ -455,6 +502,43 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
   a.tile_valid = reinterpret_cast<const int*>(ws + L.tile_valid);
   a.perm = perm;
   a.reordered = &ctrl->reordered;
+  if (opt.policy) a.row_mult = zy;  // written by the combine step once it has read the target logits
+  TeacherArgs t{};
+  if (opt.teacher) {
+    const TeacherIn& in = *opt.teacher;
+    const ListLayout E = list_layout(N, in.K, L.total);
+    t.ids = in.ids;
+    t.u = in.logits;
+    t.u_dtype = in.dtype;
+    t.K = in.K;
+    t.N = a.N;
+    t.V = a.V;
+    t.ignore_index = ignore_index;
+    t.teacher_lse = in.lse;
+    t.inv_T = 1.0 / in.temperature;
+    t.kd = in.kd;
+    t.ce = in.ce;
+    t.perm = perm;
+    t.y = y_perm;
+    t.list_ids = reinterpret_cast<int32_t*>(ws + E.ids);
+    t.list_c = reinterpret_cast<float*>(ws + E.c);
+    t.list_z = reinterpret_cast<float*>(ws + E.z);
+    t.list_count = reinterpret_cast<int*>(ws + E.count);
+    t.list_dense = reinterpret_cast<float*>(ws + E.dense);
+    t.list_const = reinterpret_cast<double*>(ws + E.kconst);
+    t.list_lse = reinterpret_cast<double*>(ws + E.klse);
+    t.list_dot = reinterpret_cast<double*>(ws + E.kdot);
+    t.status = d_status;
+    a.list_ids = t.list_ids;
+    a.list_c = t.list_c;
+    a.list_z = t.list_z;
+    a.list_count = t.list_count;
+    a.list_dense = t.list_dense;
+    a.list_stride = in.K + 1;
+    a.zs = static_cast<float>(1.0 / (LN2 * in.temperature));
+  }
+  const auto pass1 = opt.teacher ? flce_pass1_kernel<true> : flce_pass1_kernel<false>;
+  const auto pass2 = opt.teacher ? flce_pass2_kernel<true> : flce_pass2_kernel<false>;
 
   // Valid rows per 256-row token tile, then the token-row order of both passes.
   {
@@ -482,6 +566,16 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     }
   }
 
+  // The rows' lists of a distillation call.
+  if (opt.teacher) {
+    const int grid = static_cast<int>(std::min<int64_t>(N, static_cast<int64_t>(di.num_sms) * 64));
+    size_t slot;
+    prof_begin(stream, KIND_TEACHER, &slot);
+    flce_teacher_lists_kernel<<<grid, TEACHER_THREADS, static_cast<size_t>(t.K + 1) * 8, stream>>>(t);
+    prof_end(stream, slot);
+    if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
+  }
+
   // Pass 1: logits tile by tile, online log-sum-exp per (row, split); a call
   // given every vocabulary shard's statistics has its lse already.
   int total_splits = P.splits;
@@ -494,7 +588,7 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     p1.num_units = P.tiles_m * P.splits;
     size_t slot;
     prof_begin(stream, KIND_LSE, &slot);
-    flce_pass1_kernel<<<CLUSTER * P.lse_clusters, NUM_THREADS, P1_SMEM_BYTES, stream>>>(mX_k, mXc_k, mW_k, p1);
+    pass1<<<CLUSTER * P.lse_clusters, NUM_THREADS, P1_SMEM_BYTES, stream>>>(mX_k, mXc_k, mW_k, p1);
     prof_end(stream, slot);
     if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
   } else if (opt.combine != COMBINE_SHARDS_IN) {
@@ -519,10 +613,18 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
       if (cudaStreamWaitEvent(stream, pp.w_ready[i], 0) != cudaSuccess) return cuda_fail(__LINE__);
       size_t slot;
       prof_begin(stream, KIND_LSE, &slot);
-      flce_pass1_kernel<<<CLUSTER * grid, NUM_THREADS, P1_SMEM_BYTES, stream>>>(mX_k, mXc_k, mWp, p1);
+      pass1<<<CLUSTER * grid, NUM_THREADS, P1_SMEM_BYTES, stream>>>(mX_k, mXc_k, mWp, p1);
       prof_end(stream, slot);
       if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
     }
+  }
+  if (opt.teacher) {
+    const int grid = static_cast<int>(std::min<int64_t>((N + 7) / 8, static_cast<int64_t>(di.num_sms) * 8));
+    size_t slot;
+    prof_begin(stream, KIND_TEACHER, &slot);
+    flce_list_dot_kernel<<<grid, 256, 0, stream>>>(t);
+    prof_end(stream, slot);
+    if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
   }
   // Combine the splits: lse, loss, n_valid, 1/n.
   {
@@ -554,6 +656,17 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     c.all_zy = opt.all_zy;
     c.shard_lse = opt.shard_lse;
     c.shard_zy = opt.shard_zy;
+    if (opt.policy) {
+      c.policy = true;
+      c.pol = *opt.policy;
+      c.logp = opt.logp;
+      c.row_mult = zy;
+    }
+    if (opt.teacher) {
+      c.list_const = t.list_const;
+      c.list_lse = t.list_lse;
+      c.list_dot = t.list_dot;
+    }
     const int grid = static_cast<int>((N + COMBINE_THREADS - 1) / COMBINE_THREADS);
     size_t slot;
     prof_begin(stream, KIND_COMBINE, &slot);
@@ -625,7 +738,7 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
       const int grid = static_cast<int>(std::min<long long>(b.item_end - b.item_begin, P.clusters));
       if (grid > 0) {
         prof_begin(stream, KIND_PASS2, &slot);
-        flce_pass2_kernel<<<CLUSTER * grid, NUM_THREADS, SMEM_BYTES, stream>>>(pm, b);
+        pass2<<<CLUSTER * grid, NUM_THREADS, SMEM_BYTES, stream>>>(pm, b);
         prof_end(stream, slot);
         if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
       }
@@ -675,6 +788,128 @@ flce_status_t sync_call(const uint16_t* X, const uint16_t* W, const int32_t* y, 
   if (cudaStreamSynchronize(stream) != cudaSuccess) return cuda_fail(__LINE__);
   *loss = host.loss;
   return static_cast<flce_status_t>(host.status);
+}
+
+// ---------------------------------------------------- post-training losses --
+flce_status_t check_reduction(int32_t r) {
+  return r == FLCE_REDUCTION_MEAN || r == FLCE_REDUCTION_SUM || r == FLCE_REDUCTION_NONE ? FLCE_OK
+                                                                                       : FLCE_ERR_INVALID_ARGUMENT;
+}
+
+bool is_finite(double x) { return x - x == 0.0; }
+
+// The policy loss's clip widths and KL weight.
+flce_status_t check_policy(double clip_low, double clip_high, double kl_coef, const float* d_ref_logp) {
+  if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(clip_high >= 0.0) || !is_finite(kl_coef)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (kl_coef != 0.0 && !d_ref_logp) return FLCE_ERR_INVALID_ARGUMENT;
+  return FLCE_OK;
+}
+
+PolicyArgs policy_args(const float* old_logp, const float* adv, const float* ref_logp, double clip_low,
+                       double clip_high, double kl_coef) {
+  PolicyArgs p{};
+  p.old_logp = old_logp;
+  p.adv = adv;
+  p.ref_logp = ref_logp;
+  p.lo = 1.0 - clip_low;
+  p.hi = 1.0 + clip_high;
+  p.kl_coef = kl_coef;
+  return p;
+}
+
+size_t dtype_bytes(int32_t dtype) {
+  return dtype == FLCE_DTYPE_FP32 ? 4 : dtype == FLCE_DTYPE_BF16 || dtype == FLCE_DTYPE_FP16 ? 2 : 0;
+}
+
+flce_status_t check_teacher(const int32_t* ids, const void* logits, int32_t dtype, int32_t K, const float* lse,
+                            double temperature, double kd, double ce) {
+  if (!ids || !logits || K <= 0 || K > DISTILL_MAX_K || dtype_bytes(dtype) == 0) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!(temperature > 0.0) || !is_finite(temperature) || !is_finite(1.0 / temperature) || !is_finite(kd) || !is_finite(ce))
+    return FLCE_ERR_INVALID_ARGUMENT;
+  if (!aligned(ids, 4) || !aligned(logits, dtype_bytes(dtype)) || !aligned(lse, 4)) return FLCE_ERR_UNSUPPORTED;
+  return FLCE_OK;
+}
+
+// Logits of one of the three types with a row stride, and a gradient that is
+// either the logits themselves (in place) or does not touch their memory.
+flce_status_t check_logits(const void* logits, int32_t dtype, int64_t ld, int64_t N, int64_t V, const void* grad,
+                           int64_t ld_grad) {
+  const size_t es = dtype_bytes(dtype);
+  if (!logits || es == 0) return FLCE_ERR_INVALID_ARGUMENT;
+  if (N <= 0 || V <= 0 || N > (1ll << 30) || V > (1ll << 30)) return FLCE_ERR_INVALID_ARGUMENT;
+  if (ld < V || ld > (1ll << 31) || (grad && (ld_grad < V || ld_grad > (1ll << 31)))) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!aligned(logits, es) || !aligned(grad, es)) return FLCE_ERR_UNSUPPORTED;
+  if (grad == logits && ld_grad != ld) return FLCE_ERR_INVALID_ARGUMENT;
+  if (grad && grad != logits) {
+    const uint8_t* z0 = static_cast<const uint8_t*>(logits);
+    const uint8_t* g0 = static_cast<const uint8_t*>(grad);
+    const uint8_t* z1 = z0 + static_cast<size_t>((N - 1) * ld + V) * es;
+    const uint8_t* g1 = g0 + static_cast<size_t>((N - 1) * ld_grad + V) * es;
+    if (z0 < g1 && g0 < z1) return FLCE_ERR_INVALID_ARGUMENT;
+  }
+  return FLCE_OK;
+}
+
+// Rows up to which one CTA counts the valid ones.
+constexpr int64_t BEGIN_MAX_ROWS = 32768;
+
+// Zeroes the call's counters and status and counts its valid rows into the
+// control block of a ce_ws_layout workspace.
+flce_status_t begin_rows(const int32_t* y, int64_t N, int32_t ignore_index, uint8_t* ws, const CeLayout& L,
+                         int32_t* d_status, cudaStream_t stream) {
+  unsigned int* ticket = reinterpret_cast<unsigned int*>(ws + L.ctrl + 4);
+  int* n_valid = reinterpret_cast<int*>(ws + L.ctrl + 8);
+  size_t slot;
+  if (N <= BEGIN_MAX_ROWS) {
+    prof_begin(stream, KIND_PREP, &slot);
+    flce_begin_kernel<<<1, BEGIN_THREADS, 0, stream>>>(y, static_cast<int>(N), ignore_index, ticket, n_valid,
+                                                       d_status);
+  } else {
+    if (cudaMemsetAsync(ws + L.ctrl, 0, 256, stream) != cudaSuccess ||
+        cudaMemsetAsync(d_status, 0, sizeof(int32_t), stream) != cudaSuccess)
+      return cuda_fail(__LINE__);
+    prof_begin(stream, KIND_PREP, &slot);
+    flce_prep_kernel<<<static_cast<int>((N + CM - 1) / CM), CM, 0, stream>>>(y, static_cast<int>(N), ignore_index,
+                                                                           nullptr, n_valid);
+  }
+  prof_end(stream, slot);
+  return cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
+}
+
+template <int LOSS>
+void launch_logit_loss(const LogitArgs& a, int dtype, int num_sms, size_t smem, cudaStream_t stream) {
+  const int grid = static_cast<int>(std::min<int64_t>(a.N, static_cast<int64_t>(num_sms) * 256));
+  if (dtype == FLCE_DTYPE_BF16)
+    flce_logit_loss_kernel<__nv_bfloat16, LOSS><<<grid, LOGIT_THREADS, smem, stream>>>(a);
+  else if (dtype == FLCE_DTYPE_FP16)
+    flce_logit_loss_kernel<__half, LOSS><<<grid, LOGIT_THREADS, smem, stream>>>(a);
+  else
+    flce_logit_loss_kernel<float, LOSS><<<grid, LOGIT_THREADS, smem, stream>>>(a);
+}
+
+// What the two losses on logits share: device check, counters, launch.
+flce_status_t enqueue_logit_loss(LogitArgs& a, int loss, int32_t dtype, uint8_t* ws, cudaStream_t stream) {
+  DevInfo di;
+  int dev;
+  if (device_info(&di, &dev) != cudaSuccess) return cuda_fail(__LINE__);
+  if (!di.sm100) return FLCE_ERR_UNSUPPORTED;
+  const CeLayout L = ce_ws_layout(a.N);
+  const flce_status_t s = begin_rows(a.y, a.N, a.ignore_index, ws, L, a.status, stream);
+  if (s != FLCE_OK) return s;
+  a.ticket = reinterpret_cast<unsigned int*>(ws + L.ctrl + 4);
+  a.n_valid = reinterpret_cast<const int*>(ws + L.ctrl + 8);
+  a.row_acc = reinterpret_cast<double*>(ws + L.row_acc);
+  const size_t smem = 16 * (loss == LOSS_POLICY ? 1 : static_cast<size_t>(a.K) + 1);
+  size_t slot;
+  prof_begin(stream, KIND_LOGIT_LOSS, &slot);
+  if (loss == LOSS_POLICY)
+    launch_logit_loss<LOSS_POLICY>(a, dtype, di.num_sms, smem, stream);
+  else if (loss == LOSS_DISTILL)
+    launch_logit_loss<LOSS_DISTILL>(a, dtype, di.num_sms, smem, stream);
+  else
+    launch_logit_loss<LOSS_DISTILL2>(a, dtype, di.num_sms, smem, stream);
+  prof_end(stream, slot);
+  return cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
 }
 
 }  // namespace
@@ -877,6 +1112,219 @@ flce_status_t flce_pairwise_logistic(const float* d_row_loss, const int32_t* y, 
   if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
   flce_pref_weights_kernel<<<S, PREF_THREADS, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
+}
+
+flce_status_t flce_clipped_policy(const float* d_row_loss, const int32_t* y, int64_t N, int32_t ignore_index,
+                                  const float* d_old_logp, const float* d_advantage, const float* d_ref_logp,
+                                  double clip_low, double clip_high, double kl_coef, int32_t reduction,
+                                  const float* d_row_scale, double* d_loss, float* d_policy_loss, float* d_kl,
+                                  float* d_row_weight, int32_t* d_status, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+  if (!d_row_loss || !y || !d_advantage || !d_loss || !d_policy_loss || !d_kl || !d_row_weight || !d_status ||
+      !workspace || N <= 0 || N > (1ll << 30))
+    return FLCE_ERR_INVALID_ARGUMENT;
+  flce_status_t s = check_reduction(reduction);
+  if (s == FLCE_OK) s = check_policy(clip_low, clip_high, kl_coef, d_ref_logp);
+  if (s != FLCE_OK) return s;
+  for (const void* p : {static_cast<const void*>(d_row_loss), static_cast<const void*>(y),
+                        static_cast<const void*>(d_old_logp), static_cast<const void*>(d_advantage),
+                        static_cast<const void*>(d_ref_logp), static_cast<const void*>(d_row_scale),
+                        static_cast<const void*>(d_policy_loss), static_cast<const void*>(d_kl),
+                        static_cast<const void*>(d_row_weight), static_cast<const void*>(d_status)})
+    if (!aligned(p, 4)) return FLCE_ERR_UNSUPPORTED;
+  if (!aligned(d_loss, 8) || !aligned(workspace, 256)) return FLCE_ERR_UNSUPPORTED;
+  const CeLayout L = ce_ws_layout(N);
+  if (workspace_bytes < L.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  DevInfo di;
+  int dev;
+  if (device_info(&di, &dev) != cudaSuccess) return cuda_fail(__LINE__);
+  if (!di.sm100) return FLCE_ERR_UNSUPPORTED;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  s = begin_rows(y, N, ignore_index, ws, L, d_status, stream);
+  if (s != FLCE_OK) return s;
+  PolicyRowsArgs a{};
+  a.pol = policy_args(d_old_logp, d_advantage, d_ref_logp, clip_low, clip_high, kl_coef);
+  a.row_loss = d_row_loss;
+  a.y = y;
+  a.N = static_cast<int>(N);
+  a.ignore_index = ignore_index;
+  a.reduction = reduction;
+  a.row_scale = reduction == FLCE_REDUCTION_NONE ? d_row_scale : nullptr;
+  a.n_valid = reinterpret_cast<const int*>(ws + L.ctrl + 8);
+  a.ticket = reinterpret_cast<unsigned int*>(ws + L.ctrl + 4);
+  a.blk_sum = reinterpret_cast<double*>(ws + L.row_acc);
+  a.loss = d_loss;
+  a.out_rows = d_policy_loss;
+  a.out_kl = d_kl;
+  a.out_weight = d_row_weight;
+  const int grid = static_cast<int>(
+      std::min<int64_t>((N + POLICY_THREADS - 1) / POLICY_THREADS, static_cast<int64_t>(di.num_sms) * 8));
+  size_t slot;
+  prof_begin(stream, KIND_POLICY_ROWS, &slot);
+  flce_policy_rows_kernel<<<grid, POLICY_THREADS, 0, stream>>>(a);
+  prof_end(stream, slot);
+  return cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
+}
+
+flce_status_t flce_policy_loss(const void* logits, int32_t dtype, int64_t ld, const int32_t* y, int64_t N, int64_t V,
+                               int32_t ignore_index, double temperature, const float* d_old_logp,
+                               const float* d_advantage, const float* d_ref_logp, double clip_low, double clip_high,
+                               double kl_coef, double entropy_coef, int32_t reduction, const float* grad_row_scale,
+                               float* d_loss, float* d_logp, float* d_entropy, float* d_kl, int32_t* d_status,
+                               void* dlogits, int64_t ld_dlogits, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream) {
+  flce_status_t s = check_logits(logits, dtype, ld, N, V, dlogits, ld_dlogits);
+  if (s == FLCE_OK) s = check_reduction(reduction);
+  if (s == FLCE_OK) s = check_policy(clip_low, clip_high, kl_coef, d_ref_logp);
+  if (s != FLCE_OK) return s;
+  if (!y || !d_advantage || !d_loss || !d_logp || !d_entropy || !d_kl || !d_status || !workspace)
+    return FLCE_ERR_INVALID_ARGUMENT;
+  if (!(temperature > 0.0) || !is_finite(temperature) || !is_finite(1.0 / temperature) || !is_finite(entropy_coef))
+    return FLCE_ERR_INVALID_ARGUMENT;
+  for (const void* p : {static_cast<const void*>(y), static_cast<const void*>(d_old_logp),
+                        static_cast<const void*>(d_advantage), static_cast<const void*>(d_ref_logp),
+                        static_cast<const void*>(grad_row_scale), static_cast<const void*>(d_loss),
+                        static_cast<const void*>(d_logp), static_cast<const void*>(d_entropy),
+                        static_cast<const void*>(d_kl), static_cast<const void*>(d_status)})
+    if (!aligned(p, 4)) return FLCE_ERR_UNSUPPORTED;
+  if (!aligned(workspace, 256)) return FLCE_ERR_UNSUPPORTED;
+  if (workspace_bytes < ce_ws_layout(N).total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  LogitArgs a{};
+  a.z = logits;
+  a.g = dlogits;
+  a.ld = ld;
+  a.ldg = ld_dlogits;
+  a.y = y;
+  a.N = static_cast<int>(N);
+  a.V = static_cast<int>(V);
+  a.ignore_index = ignore_index;
+  a.reduction = reduction;
+  a.row_scale = reduction == FLCE_REDUCTION_NONE ? grad_row_scale : nullptr;
+  a.loss = d_loss;
+  a.status = d_status;
+  a.inv_T = 1.0 / temperature;
+  a.zs = static_cast<float>(1.0 / (LN2 * temperature));
+  a.pol = policy_args(d_old_logp, d_advantage, d_ref_logp, clip_low, clip_high, kl_coef);
+  a.ent_coef = entropy_coef;
+  a.out_logp = d_logp;
+  a.out_entropy = d_entropy;
+  a.out_kl = d_kl;
+  return enqueue_logit_loss(a, LOSS_POLICY, dtype, static_cast<uint8_t*>(workspace), stream);
+}
+
+flce_status_t flce_distill_topk(const void* logits, int32_t dtype, int64_t ld, const int32_t* y, int64_t N, int64_t V,
+                                int32_t ignore_index, const int32_t* d_teacher_ids, const void* d_teacher_logits,
+                                int32_t teacher_dtype, int32_t K, const float* d_teacher_lse, double temperature,
+                                double kd_weight, double ce_weight, int32_t reduction, const float* grad_row_scale,
+                                float* d_loss, float* d_row_loss, int32_t* d_status, void* dlogits,
+                                int64_t ld_dlogits, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  flce_status_t s = check_logits(logits, dtype, ld, N, V, dlogits, ld_dlogits);
+  if (s == FLCE_OK) s = check_reduction(reduction);
+  if (s == FLCE_OK)
+    s = check_teacher(d_teacher_ids, d_teacher_logits, teacher_dtype, K, d_teacher_lse, temperature, kd_weight,
+                      ce_weight);
+  if (s != FLCE_OK) return s;
+  if (!y || !d_loss || !d_status || !workspace) return FLCE_ERR_INVALID_ARGUMENT;
+  if (!aligned(y, 4) || !aligned(grad_row_scale, 4) || !aligned(d_loss, 4) || !aligned(d_row_loss, 4) ||
+      !aligned(d_status, 4) || !aligned(workspace, 256))
+    return FLCE_ERR_UNSUPPORTED;
+  if (workspace_bytes < ce_ws_layout(N).total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  LogitArgs a{};
+  a.z = logits;
+  a.g = dlogits;
+  a.ld = ld;
+  a.ldg = ld_dlogits;
+  a.y = y;
+  a.N = static_cast<int>(N);
+  a.V = static_cast<int>(V);
+  a.ignore_index = ignore_index;
+  a.reduction = reduction;
+  a.row_scale = reduction == FLCE_REDUCTION_NONE ? grad_row_scale : nullptr;
+  a.loss = d_loss;
+  a.status = d_status;
+  a.inv_T = 1.0 / temperature;
+  a.zs = static_cast<float>(1.0 / (LN2 * temperature));
+  a.ids = d_teacher_ids;
+  a.u = d_teacher_logits;
+  a.u_dtype = teacher_dtype;
+  a.K = K;
+  a.teacher_lse = d_teacher_lse;
+  a.kd = kd_weight;
+  a.ce = ce_weight;
+  a.out_rows = d_row_loss;
+  return enqueue_logit_loss(a, temperature != 1.0 && ce_weight != 0.0 ? LOSS_DISTILL2 : LOSS_DISTILL, dtype,
+                            static_cast<uint8_t*>(workspace), stream);
+}
+
+flce_status_t flce_policy_forward_backward(const uint16_t* X, const uint16_t* W, const int32_t* y, int64_t N,
+                                           int64_t H, int64_t V, int32_t ignore_index, const float* d_old_logp,
+                                           const float* d_advantage, const float* d_ref_logp, double clip_low,
+                                           double clip_high, double kl_coef, int32_t reduction,
+                                           const float* grad_row_scale, const int32_t* d_mean_count, float* d_loss,
+                                           float* d_logp, int32_t* d_status, uint16_t* dX, uint16_t* dW,
+                                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!d_advantage || !d_loss || !d_logp || !d_status) return FLCE_ERR_INVALID_ARGUMENT;
+  flce_status_t s = check_reduction(reduction);
+  if (s == FLCE_OK) s = check_policy(clip_low, clip_high, kl_coef, d_ref_logp);
+  if (s == FLCE_OK) s = check_args(X, W, y, N, H, V, dX, dW, workspace, true);
+  if (s != FLCE_OK) return s;
+  for (const void* p : {static_cast<const void*>(d_old_logp), static_cast<const void*>(d_advantage),
+                        static_cast<const void*>(d_ref_logp), static_cast<const void*>(grad_row_scale),
+                        static_cast<const void*>(d_mean_count), static_cast<const void*>(d_loss),
+                        static_cast<const void*>(d_logp), static_cast<const void*>(d_status)})
+    if (!aligned(p, 4)) return FLCE_ERR_UNSUPPORTED;
+  if (workspace_bytes < ws_layout(N, H).total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  const PolicyArgs pol = policy_args(d_old_logp, d_advantage, d_ref_logp, clip_low, clip_high, kl_coef);
+  Options opt;
+  opt.reduction = reduction;
+  opt.grad_row_scale = reduction == FLCE_REDUCTION_NONE ? grad_row_scale : nullptr;
+  opt.mean_count = reduction == FLCE_REDUCTION_MEAN ? d_mean_count : nullptr;
+  opt.policy = &pol;
+  opt.logp = d_logp;
+  return enqueue(X, W, y, N, H, V, ignore_index, d_loss, d_status, dX, dW, workspace, workspace_bytes, stream, opt);
+}
+
+size_t flce_distill_workspace_size(int64_t N, int64_t H, int32_t K, int32_t reorder) {
+  if (check_sizes(N, H, 1) != FLCE_OK || K <= 0 || K > DISTILL_MAX_K) return 0;
+  return list_layout(N, K, ws_layout(N, H, reorder != 0).total).total;
+}
+
+flce_status_t flce_distill_forward_backward(const uint16_t* X, const uint16_t* W, const int32_t* y, int64_t N,
+                                            int64_t H, int64_t V, int32_t ignore_index, const int32_t* d_teacher_ids,
+                                            const void* d_teacher_logits, int32_t teacher_dtype, int32_t K,
+                                            const float* d_teacher_lse, double temperature, double kd_weight,
+                                            double ce_weight, int32_t reduction, const float* grad_row_scale,
+                                            const int32_t* d_mean_count, float* d_loss, float* d_row_loss,
+                                            int32_t* d_status, uint16_t* dX, uint16_t* dW, void* workspace,
+                                            size_t workspace_bytes, cudaStream_t stream) {
+  if (!d_loss || !d_status) return FLCE_ERR_INVALID_ARGUMENT;
+  flce_status_t s = check_reduction(reduction);
+  if (s == FLCE_OK)
+    s = check_teacher(d_teacher_ids, d_teacher_logits, teacher_dtype, K, d_teacher_lse, temperature, kd_weight,
+                      ce_weight);
+  if (s == FLCE_OK) s = check_args(X, W, y, N, H, V, dX, dW, workspace, true);
+  if (s != FLCE_OK) return s;
+  if (temperature != 1.0 && ce_weight != 0.0) return FLCE_ERR_UNSUPPORTED;  // one softmax per logit tile
+  if (!aligned(grad_row_scale, 4) || !aligned(d_mean_count, 4) || !aligned(d_loss, 4) || !aligned(d_row_loss, 4) ||
+      !aligned(d_status, 4))
+    return FLCE_ERR_UNSUPPORTED;
+  if (workspace_bytes < flce_distill_workspace_size(N, H, K, 0)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  TeacherIn t{};
+  t.ids = d_teacher_ids;
+  t.logits = d_teacher_logits;
+  t.dtype = teacher_dtype;
+  t.K = K;
+  t.lse = d_teacher_lse;
+  t.temperature = temperature;
+  t.kd = kd_weight;
+  t.ce = ce_weight;
+  Options opt;
+  opt.reduction = reduction;
+  opt.grad_row_scale = reduction == FLCE_REDUCTION_NONE ? grad_row_scale : nullptr;
+  opt.row_loss = d_row_loss;
+  opt.mean_count = reduction == FLCE_REDUCTION_MEAN ? d_mean_count : nullptr;
+  opt.teacher = &t;
+  return enqueue(X, W, y, N, H, V, ignore_index, d_loss, d_status, dX, dW, workspace, workspace_bytes, stream, opt);
 }
 
 namespace {
@@ -1096,6 +1544,9 @@ const char* flce_kernel_name(int kind) {
     case KIND_PACK: return "prep_pack_rows";
     case KIND_H2D: return "copy_host_to_device";
     case KIND_D2H: return "copy_device_to_host";
+    case KIND_LOGIT_LOSS: return "logit_loss_rows";
+    case KIND_POLICY_ROWS: return "policy_rows";
+    case KIND_TEACHER: return "teacher_lists";
     default: return "unknown";
   }
 }

@@ -40,6 +40,7 @@
 #include <cfloat>
 #include <cstdint>
 
+#include "policy.cuh"
 #include "sm100.cuh"
 
 namespace flce {
@@ -111,7 +112,8 @@ __host__ __device__ __forceinline__ int target_elsewhere(int ignore_index) {
 // Kinds of launch, as the profiler reports them.
 enum : int {
   KIND_LSE = 0, KIND_COMBINE = 1, KIND_PASS2 = 2, KIND_PREP = 3, KIND_CE = 4, KIND_ORDER = 5, KIND_SCATTER = 6,
-  KIND_PACK = 7, KIND_H2D = 8, KIND_D2H = 9  // the last two: copies of the host-buffer entry (profiling only)
+  KIND_PACK = 7, KIND_H2D = 8, KIND_D2H = 9,  // the last two: copies of the host-buffer entry (profiling only)
+  KIND_LOGIT_LOSS = 10, KIND_POLICY_ROWS = 11, KIND_TEACHER = 12  // post-training losses (in the timeline only)
 };
 enum : int { ST_TARGET_OUT_OF_RANGE = 4, ST_TIMEOUT = 5 };
 
@@ -140,6 +142,17 @@ struct GemmArgs {
   int g_cols_first;       // G(c): this many vocabulary tiles first, column by column; the rest row by row
   int reduction;                 // RED_MEAN, RED_SUM, RED_NONE
   const float* grad_row_scale;   // RED_NONE: per-row upstream gradient, or null for 1
+  const float* row_mult;         // a further factor of each row's G (derivative of a loss of l_i), or null
+  // Distillation (the kernels' LIST instantiations): each row's entries of the
+  // vocabulary where G is not the softmax alone, ascending by id, and the
+  // softmax taken at a temperature
+  const int32_t* list_ids;       // [N][list_stride]
+  const float* list_c;           // [N][list_stride] coefficient subtracted there (times the row's weight)
+  float* list_z;                 // [N][list_stride] the logit there (pass 1 writes it)
+  const int* list_count;         // [N]
+  const float* list_dense;       // [N] factor of the softmax in G (times the row's weight)
+  int list_stride;
+  float zs;                      // log2(e) / temperature
   const int* tile_valid;         // [ceil(N/256)] valid rows per 256-row token tile (prep kernel)
   // Token-row order.  When the rows of ignored targets are scattered, the rows
   // are reordered so that every valid row comes first (a stable partition);
@@ -201,15 +214,49 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int k) {
 
 // ------------------------------------------------------------- epilogues --
 
+// A walk along one row's list of vocabulary entries, in step with the columns
+// that an epilogue reads.
+struct ListWalk {
+  size_t base;    // the row's first slot
+  int pos, end;
+  int next;       // vocabulary id of the entry at pos (INT_MAX: none left)
+};
+
+// The row's first entry at or behind column col0 (binary search).
+__device__ __forceinline__ ListWalk list_begin(const GemmArgs& a, int row, bool has, int col0) {
+  ListWalk w;
+  w.base = static_cast<size_t>(row) * a.list_stride;
+  w.end = has ? a.list_count[row] : 0;
+  int lo = 0, hi = w.end;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.list_ids[w.base + mid] < col0)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  w.pos = lo;
+  w.next = lo < w.end ? a.list_ids[w.base + lo] : 0x7fffffff;
+  return w;
+}
+
+__device__ __forceinline__ void list_step(const GemmArgs& a, ListWalk& w) {
+  ++w.pos;
+  w.next = w.pos < w.end ? a.list_ids[w.base + w.pos] : 0x7fffffff;
+}
+
 struct LseState {
   float run_m, run_l, zy_val;
   int yr, row;
   bool has_zy;
+  ListWalk list;  // LIST only
 };
 
 // Pass 1: fold one [128 x 256] logit tile into the running (max, sum) of the row.
+template <bool LIST>
 __device__ __forceinline__ void epi_lse_tile(const GemmArgs& a, uint32_t taddr, int nb, LseState& st) {
   const int col_base = nb * BN;
+  const float zs = LIST ? a.zs : LOG2E;
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
     uint32_t r[32];
@@ -224,11 +271,23 @@ __device__ __forceinline__ void epi_lse_tile(const GemmArgs& a, uint32_t taddr, 
         if (t == off) st.zy_val = __uint_as_float(r[t]);
       st.has_zy = true;
     }
+    if constexpr (LIST) {
+      while (st.list.next < col0 + 32) {
+        const int o = st.list.next - col0;
+        float z = 0.f;
+#pragma unroll
+        for (int t = 0; t < 32; ++t)
+          if (t == o) z = __uint_as_float(r[t]);
+        a.list_z[st.list.base + st.list.pos] = z;
+        list_step(a, st.list);
+      }
+      __syncwarp();
+    }
     float s[32];
     float cmax = -INFINITY;
 #pragma unroll
     for (int t = 0; t < 32; ++t) {
-      s[t] = (t < lim) ? __uint_as_float(r[t]) * LOG2E : -INFINITY;
+      s[t] = (t < lim) ? __uint_as_float(r[t]) * zs : -INFINITY;
       cmax = fmaxf(cmax, s[t]);
     }
     const float new_m = fmaxf(st.run_m, cmax);
@@ -295,6 +354,7 @@ __device__ __forceinline__ void stage_and_store(EpiStage& es, int lane, const CU
 }
 
 // Pass 2: G = valid * (softmax - onehot) / n for one tile, stored as bf16.
+template <bool LIST>
 __device__ __forceinline__ void epi_grad_tile(const GemmArgs& a, int vbase, uint32_t taddr, int row0, int nb,
                                               int row_local, EpiStage& es, const CUtensorMap* mapG) {
   const int row = row0 + row_local;
@@ -303,7 +363,12 @@ __device__ __forceinline__ void epi_grad_tile(const GemmArgs& a, int vbase, uint
   const int yr = in_rows ? a.y[row] : a.ignore_index;
   const bool valid = in_rows && yr != a.ignore_index;
   const float l2 = valid ? a.lse2[row] : 0.f;
-  const float scale = valid ? row_weight(a.reduction, a.inv_n, a.grad_row_scale, row) : 0.f;
+  float scale = valid ? row_weight(a.reduction, a.inv_n, a.grad_row_scale, row) : 0.f;
+  if (a.row_mult && valid) scale *= a.row_mult[row];
+  const float zs = LIST ? a.zs : LOG2E;
+  const float dense = LIST && valid ? scale * a.list_dense[row] : scale;
+  ListWalk walk;
+  if constexpr (LIST) walk = list_begin(a, row, valid, vbase + nb * BN);
   const int wrow0 = row0 + (row_local & ~31);
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
@@ -315,12 +380,24 @@ __device__ __forceinline__ void epi_grad_tile(const GemmArgs& a, int vbase, uint
     stage_and_store(es, lane, mapG, nb * BN + c * 32, wrow0, l2_evict_normal(), [&](float (&g)[32]) {
 #pragma unroll
       for (int t = 0; t < 32; ++t)
-        g[t] = (valid && t < lim) ? ex2_approx(fmaf(__uint_as_float(r[t]), LOG2E, -l2)) * scale : 0.f;
-      const int off = yr - colg0;
-      if (valid && static_cast<unsigned>(off) < 32u) {
+        g[t] = (valid && t < lim) ? ex2_approx(fmaf(__uint_as_float(r[t]), zs, -l2)) * dense : 0.f;
+      if constexpr (LIST) {
+        while (walk.next < colg0 + 32) {
+          const int o = walk.next - colg0;
+          const float sub = a.list_c[walk.base + walk.pos] * scale;
 #pragma unroll
-        for (int t = 0; t < 32; ++t)
-          if (t == off) g[t] -= scale;
+          for (int t = 0; t < 32; ++t)
+            if (t == o) g[t] -= sub;
+          list_step(a, walk);
+        }
+        __syncwarp();
+      } else {
+        const int off = yr - colg0;
+        if (valid && static_cast<unsigned>(off) < 32u) {
+#pragma unroll
+          for (int t = 0; t < 32; ++t)
+            if (t == off) g[t] -= scale;
+        }
       }
     });
   }
@@ -545,6 +622,7 @@ __device__ __forceinline__ void producer_tail(uint32_t bars, uint32_t* slots, lo
 // Pass 1: z = X W^T tile by tile; each epilogue thread folds its row's logits
 // into a running (max, sum of exponentials) over the vocabulary split of the
 // unit, and picks out the target logit.  No logit leaves the chip.
+template <bool LIST>
 __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     flce_pass1_kernel(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapXc,
                       const __grid_constant__ CUtensorMap mapW, const GemmArgs a) {
@@ -777,6 +855,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
       st.run_l = 0.f;
       st.zy_val = 0.f;
       st.has_zy = false;
+      if constexpr (LIST) st.list = list_begin(a, st.row, st.row < a.N, nb0 * BN);
       for (int nb = nb0; nb < nb1; ++nb) {
         // a pair of tiles (nb, nb + 1) sits in buffers acc and acc ^ 1, and the
         // tile after it in acc again (the issuer's sequence)
@@ -790,7 +869,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
         }
         tc_fence_after();
         const uint32_t taddr = tmem_base + lane_addr + buf * ACC_COLS;
-        epi_lse_tile(a, taddr, nb, st);
+        epi_lse_tile<LIST>(a, taddr, nb, st);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(buf == 0 ? tempty_leader0 : tempty_leader1);
@@ -950,6 +1029,7 @@ struct Pass2Maps {
   CUtensorMap Xck, Xcmn;   // the packed copy of X (reordered rows), K- and MN-major
 };
 
+template <bool LIST>
 __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     flce_pass2_kernel(const __grid_constant__ Pass2Maps m, const GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -1363,7 +1443,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
         // zero, written once by the first chunk
         if (it.kind == ITEM_DX && it.c == 0) epi_zero_tile(taddr, row0, it.b, row_local, es, &m.Hio);
       } else if (it.kind == ITEM_GRAD) {
-        epi_grad_tile(a, vbase, taddr, row0, it.b, row_local, es, &m.Go);
+        epi_grad_tile<LIST>(a, vbase, taddr, row0, it.b, row_local, es, &m.Go);
       } else if (it.kind == ITEM_DW) {
         const int nt = dw_first_tile(a, it);
         if (any_valid)
@@ -1557,6 +1637,16 @@ struct CombineArgs {
   int reduction;
   const float* grad_row_scale;
   float* row_loss;  // optional per-row losses, in the caller's row order
+  // Policy loss of the rows' log-probabilities lp = -l in place of their sum:
+  // logp (the caller's order) and row_mult (the rows' order) are its outputs
+  bool policy;
+  PolicyArgs pol;
+  float* logp;      // [N]
+  float* row_mult;  // [N] d L_i / d l_i; may be zy itself
+  // Distillation: the row's loss is list_const + list_lse lse - list_dot (all null otherwise)
+  const double* list_const;
+  const double* list_lse;
+  const double* list_dot;
   const int* perm;  // row of the caller behind each row of y, part_m, ... (token-row order)
   const int* mean_count;  // optional: divide the mean by this count instead of n_valid
   const int32_t* y;
@@ -1621,11 +1711,21 @@ __global__ void __launch_bounds__(COMBINE_THREADS) flce_combine_kernel(const Com
     double row = 0.0;
     if (valid) {
       row = static_cast<double>(l2) * LN2 - static_cast<double>(zyi);
+      if (a.list_dot) row = a.list_const[i] + a.list_lse[i] * (static_cast<double>(l2) * LN2) - a.list_dot[i];
       vi = 1;
       // mean and sum add the plain row losses (the mean divides at the end)
       li = a.reduction == RED_NONE && a.grad_row_scale ? row * static_cast<double>(a.grad_row_scale[i]) : row;
     }
     if (a.row_loss) a.row_loss[a.perm[i]] = static_cast<float>(row);
+    if (a.policy) {
+      const int src = a.perm[i];
+      a.logp[src] = static_cast<float>(-row);
+      if (valid) {
+        const PolicyRow p = policy_row(a.pol, src, -row);
+        li = a.reduction == RED_NONE && a.grad_row_scale ? p.loss * static_cast<double>(a.grad_row_scale[i]) : p.loss;
+        a.row_mult[i] = static_cast<float>(-p.dlogp);
+      }
+    }
   } else if (a.mode == COMBINE_SHARD) {
     return;
   }

@@ -1,0 +1,569 @@
+// Post-training losses on given logits, and the row steps that they share with
+// the fused head.
+//
+// The post-training part of the library the pages describe ("Liger-Kernel:
+// Triton kernels that replace HF training ops", section "Installation and the
+// one-line patch") takes the output layer's logits or its inputs and returns a
+// loss.  Two of these losses live here:
+//
+//   clipped policy loss with a KL term.  With x = z/T and lp = x_y - lse(x),
+//     r = exp(lp - old),  kl = exp(ref - lp) - (ref - lp) - 1,
+//     L = -min(r A, clip(r, 1 - lo, 1 + hi) A) + beta kl - eta H,
+//     H = lse(x) - sum_j p_j x_j                      (the row's entropy)
+//     dL/dlp = -A r [r not clipped away] + beta (1 - exp(ref - lp)) = g
+//     dL/dz_j = (g ([j == y] - p_j) + eta p_j (log p_j + H)) / T
+//
+//   distillation from a teacher's K largest logits u_k at entries t_k,
+//     q = softmax_K(u/T), or exp(u/T - lse_teacher) with the teacher's own
+//     normaliser,  Q = sum_k q_k,
+//     L = kd sum_k q_k (log q_k - log p_{t_k}) + ce (lse(z) - z_y),  p = softmax(z/T),
+//     dL/dz_j = kd/T (Q p_j - sum_{k: t_k = j} q_k) + ce (softmax(z)_j - [j == y]).
+//
+// Both gradients are a dense part that depends on the row's softmax alone and a
+// few sparse entries, so one kernel serves both.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "flce_kernels.cuh"
+
+namespace flce {
+
+constexpr int DISTILL_MAX_K = 1024;
+constexpr float NEG_BIG = -1e4f;  // exponents below this are 0 in every format; finite, so that 0 * it is 0
+
+// ------------------------------------------------------- logits by type --
+
+template <typename T>
+struct LogitTraits;
+template <>
+struct LogitTraits<__nv_bfloat16> {
+  __device__ static float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  __device__ static void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+};
+template <>
+struct LogitTraits<__half> {
+  __device__ static float load(const __half* p) { return __half2float(*p); }
+  __device__ static void store(__half* p, float v) { *p = __float2half_rn(v); }
+};
+template <>
+struct LogitTraits<float> {
+  __device__ static float load(const float* p) { return *p; }
+  __device__ static void store(float* p, float v) { *p = v; }
+};
+
+enum : int { DT_BF16 = 0, DT_FP16 = 1, DT_FP32 = 2 };
+
+__device__ __forceinline__ float load_as_f32(const void* p, int dtype, size_t i) {
+  if (dtype == DT_FP32) return static_cast<const float*>(p)[i];
+  if (dtype == DT_FP16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+// ------------------------------------------------------------ setup, sums --
+
+// Counters and the status word of a call, and its number of valid rows
+// (one CTA: short enough for the row counts it is launched for).
+constexpr int BEGIN_THREADS = 1024;
+__global__ void __launch_bounds__(BEGIN_THREADS)
+    flce_begin_kernel(const int32_t* y, int N, int ignore_index, unsigned int* ticket, int* n_valid, int* status) {
+  int c = 0;
+  for (int i = threadIdx.x; i < N; i += BEGIN_THREADS) c += y[i] != ignore_index ? 1 : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) c += __shfl_down_sync(0xffffffffu, c, o);
+  __shared__ int w[BEGIN_THREADS / 32];
+  if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = c;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int t = 0;
+    for (int k = 0; k < BEGIN_THREADS / 32; ++k) t += w[k];
+    *n_valid = t;
+    *ticket = 0u;
+    *status = 0;
+  }
+}
+
+// The last block to finish adds the rows' contributions in row order: a fixed
+// tree over a fixed assignment, in fp64.
+template <int THREADS>
+__device__ __forceinline__ double ordered_sum(const double* v, int n, double* scratch) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += THREADS) s += __ldcg(v + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = s;
+  __syncthreads();
+  double t = 0.0;
+  if (threadIdx.x == 0)
+    for (int k = 0; k < THREADS / 32; ++k) t += scratch[k];
+  return t;  // thread 0's
+}
+
+// ------------------------------------------------------ teacher's softmax --
+
+// A warp's view of one row's teacher distribution over the K entries of s_u
+// (-inf: no entry): log q_k = u_k / T - shift.  `any` is false when the row has
+// no entry.  Differences are taken in fp64 before they are rounded for expf,
+// so large teacher logits cost no precision; the sum is fp32.
+struct TeacherShift {
+  double shift;
+  bool any;
+};
+__device__ __forceinline__ TeacherShift teacher_shift(const float* s_u, int K, int lane, double inv_T,
+                                                      const float* teacher_lse, size_t row) {
+  float um = -INFINITY;
+  bool any = false;
+  for (int k = lane; k < K; k += 32) {
+    um = fmaxf(um, s_u[k]);
+    any = any || !(s_u[k] == -INFINITY);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) um = fmaxf(um, __shfl_xor_sync(0xffffffffu, um, o));
+  TeacherShift t;
+  t.any = __any_sync(0xffffffffu, any);
+  t.shift = static_cast<double>(um) * inv_T;
+  if (teacher_lse) {
+    t.shift = static_cast<double>(teacher_lse[row]);
+  } else if (t.any) {
+    float S = 0.f;
+    for (int k = lane; k < K; k += 32) S += expf(static_cast<float>(static_cast<double>(s_u[k]) * inv_T - t.shift));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+    t.shift += log(static_cast<double>(S));
+  }
+  return t;
+}
+
+// ------------------------------------------------------ clipped policy rows --
+
+struct PolicyRowsArgs {
+  PolicyArgs pol;
+  const float* row_loss;  // [N] l_i = -lp_i
+  const int32_t* y;
+  int N, ignore_index, reduction;
+  const float* row_scale;
+  const int* n_valid;
+  unsigned int* ticket;
+  double* blk_sum;      // [gridDim.x]
+  double* loss;
+  float* out_rows;      // [N] policy loss per row
+  float* out_kl;        // [N]
+  float* out_weight;    // [N] s_i dL_i/dl_i
+};
+
+constexpr int POLICY_THREADS = 256;
+__global__ void __launch_bounds__(POLICY_THREADS) flce_policy_rows_kernel(const PolicyRowsArgs a) {
+  const int n = *a.n_valid;
+  const double inv_n = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
+  double acc = 0.0;
+  for (int i = blockIdx.x * POLICY_THREADS + threadIdx.x; i < a.N; i += gridDim.x * POLICY_THREADS) {
+    float rows = 0.f, kl = 0.f, weight = 0.f;
+    if (a.y[i] != a.ignore_index) {
+      const PolicyRow p = policy_row(a.pol, i, -static_cast<double>(a.row_loss[i]));
+      const double s = a.reduction == RED_MEAN ? inv_n
+                       : a.reduction == RED_NONE && a.row_scale ? static_cast<double>(a.row_scale[i]) : 1.0;
+      rows = static_cast<float>(p.loss);
+      kl = static_cast<float>(p.kl);
+      weight = static_cast<float>(-p.dlogp * s);
+      acc += a.reduction == RED_MEAN ? p.loss : p.loss * s;
+    }
+    a.out_rows[i] = rows;
+    a.out_kl[i] = kl;
+    a.out_weight[i] = weight;
+  }
+  __shared__ double w[POLICY_THREADS / 32];
+  __shared__ bool is_last;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_down_sync(0xffffffffu, acc, o);
+  if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = acc;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+    for (int k = 0; k < POLICY_THREADS / 32; ++k) t += w[k];
+    a.blk_sum[blockIdx.x] = t;
+    __threadfence();
+    is_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!is_last) return;
+  __threadfence();
+  const double t = ordered_sum<POLICY_THREADS>(a.blk_sum, gridDim.x, w);
+  if (threadIdx.x == 0) *a.loss = a.reduction == RED_MEAN ? t * inv_n : t;
+}
+
+// --------------------------------------------------- losses on the logits --
+
+enum : int {
+  LOSS_POLICY = 0,    // clipped policy loss
+  LOSS_DISTILL = 1,   // distillation, one softmax (ce == 0 or T == 1)
+  LOSS_DISTILL2 = 2   // distillation at T != 1 mixed with hard labels: a second softmax at T = 1
+};
+
+struct LogitArgs {
+  const void* z;          // [N][V], row stride ld elements
+  void* g;                // gradient, row stride ldg, or null; may be z itself
+  long long ld, ldg;
+  const int32_t* y;
+  int N, V, ignore_index, reduction;
+  const float* row_scale;
+  const int* n_valid;
+  unsigned int* ticket;
+  double* row_acc;        // [N]
+  float* loss;
+  int* status;
+  double inv_T;
+  float zs;               // log2(e) / T
+  // policy
+  PolicyArgs pol;
+  double ent_coef;
+  float* out_logp;        // [N]
+  float* out_entropy;     // [N]
+  float* out_kl;          // [N]
+  // distillation
+  const int32_t* ids;     // [N][K], negative: no entry
+  const void* u;          // [N][K] teacher logits
+  int u_dtype, K;
+  const float* teacher_lse;  // [N] or null
+  double kd, ce;
+  float* out_rows;        // [N] or null
+};
+
+// A row's running statistics: max of z, sum of e = 2^((z - m) zs), and for the
+// policy loss the first moment sum e (z - m) zs, for DISTILL2 the sum of
+// 2^((z - m) log2 e).
+struct RowStat {
+  float m, l, t;
+};
+
+template <int LOSS>
+__device__ __forceinline__ void stat_add(RowStat& s, float z, float zs) {
+  if (z > s.m) {  // move to the new maximum
+    const float d = (s.m - z) * zs, f = ex2_approx(d);
+    if constexpr (LOSS == LOSS_POLICY) s.t = f * (s.t + s.l * fmaxf(d, NEG_BIG));
+    if constexpr (LOSS == LOSS_DISTILL2) s.t *= ex2_approx((s.m - z) * LOG2E);
+    s.l *= f;
+    s.m = z;
+  }
+  const float d = (z - s.m) * zs, e = ex2_approx(d);
+  s.l += e;
+  if constexpr (LOSS == LOSS_POLICY) s.t += e * fmaxf(d, NEG_BIG);
+  if constexpr (LOSS == LOSS_DISTILL2) s.t += ex2_approx((z - s.m) * LOG2E);
+}
+
+template <int LOSS>
+__device__ __forceinline__ void stat_merge(RowStat& s, const RowStat& o, float zs) {
+  const float m = fmaxf(s.m, o.m);
+  const float d1 = (s.m - m) * zs, d2 = (o.m - m) * zs;
+  const float f1 = ex2_approx(d1), f2 = ex2_approx(d2);
+  if constexpr (LOSS == LOSS_POLICY)
+    s.t = f1 * (s.t + s.l * fmaxf(d1, NEG_BIG)) + f2 * (o.t + o.l * fmaxf(d2, NEG_BIG));
+  if constexpr (LOSS == LOSS_DISTILL2)
+    s.t = s.t * ex2_approx((s.m - m) * LOG2E) + o.t * ex2_approx((o.m - m) * LOG2E);
+  s.l = s.l * f1 + o.l * f2;
+  s.m = m;
+}
+
+constexpr int LOGIT_THREADS = 512;
+
+// What the gradient pass needs of a row.
+struct RowCoef {
+  float m;       // the row's maximum
+  float a, b;    // dense part: e (a + b arg), or a e + b e1 with two softmaxes
+};
+
+// One CTA per row: an online pass over the row, the row's scalars, a second
+// pass that writes the gradient, then the sparse entries.
+template <typename T, int LOSS>
+__global__ void __launch_bounds__(LOGIT_THREADS) flce_logit_loss_kernel(const LogitArgs a) {
+  using L = LogitTraits<T>;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  const int K1 = LOSS == LOSS_POLICY ? 1 : a.K + 1;
+  int* s_id = reinterpret_cast<int*>(dyn);           // sparse entries' vocabulary ids (-1: none)
+  float* s_u = reinterpret_cast<float*>(s_id + K1);  // teacher logits
+  float* s_c = s_u + K1;                             // coefficient subtracted at the entry
+  float* s_z = s_c + K1;                             // the student's logit there
+  __shared__ RowStat w_stat[LOGIT_THREADS / 32];
+  __shared__ RowCoef coef;
+  __shared__ double dsum[LOGIT_THREADS / 32];
+  __shared__ bool is_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n_valid = *a.n_valid;
+  const double inv_n = n_valid > 0 ? 1.0 / static_cast<double>(n_valid) : 0.0;
+  for (int row = blockIdx.x; row < a.N; row += gridDim.x) {
+    const T* z = static_cast<const T*>(a.z) + static_cast<long long>(row) * a.ld;
+    T* g = a.g ? static_cast<T*>(a.g) + static_cast<long long>(row) * a.ldg : nullptr;
+    const int y = a.y[row];
+    const bool in_range = y >= 0 && y < a.V;
+    if (y == a.ignore_index || !in_range) {
+      if (tid == 0) {
+        if (y != a.ignore_index) raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
+        a.row_acc[row] = 0.0;
+        if constexpr (LOSS == LOSS_POLICY) {
+          a.out_logp[row] = a.out_entropy[row] = a.out_kl[row] = 0.f;
+        } else if (a.out_rows) {
+          a.out_rows[row] = 0.f;
+        }
+      }
+      if (g)
+        for (int j = tid; j < a.V; j += LOGIT_THREADS) L::store(g + j, 0.f);
+      continue;
+    }
+    // the sparse entries: the teacher's, then the target
+    for (int k = tid; k < K1; k += LOGIT_THREADS) {
+      int id = y;
+      float u = -INFINITY;
+      if (k < K1 - 1) {
+        const size_t at = static_cast<size_t>(row) * a.K + k;
+        id = a.ids[at];
+        if (id >= a.V) {
+          raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
+          id = -1;
+        }
+        if (id >= 0) u = load_as_f32(a.u, a.u_dtype, at);
+      }
+      s_id[k] = id < 0 ? -1 : id;
+      s_u[k] = u;
+      s_z[k] = id < 0 ? 0.f : L::load(z + id);
+    }
+    RowStat st{-FLT_MAX, 0.f, 0.f};
+    for (int j = tid; j < a.V; j += LOGIT_THREADS) stat_add<LOSS>(st, L::load(z + j), a.zs);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      RowStat other;
+      other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+      other.l = __shfl_xor_sync(0xffffffffu, st.l, o);
+      other.t = __shfl_xor_sync(0xffffffffu, st.t, o);
+      stat_merge<LOSS>(st, other, a.zs);
+    }
+    if (lane == 0) w_stat[warp] = st;
+    __syncthreads();
+    if (warp == 0) {
+      st = w_stat[0];
+      for (int w = 1; w < LOGIT_THREADS / 32; ++w) stat_merge<LOSS>(st, w_stat[w], a.zs);
+      // Log-probabilities as (z - m)/T - ln L: the difference first, so that a
+      // row whose every logit is the type's lowest value still has one.
+      const double m = static_cast<double>(st.m);
+      const double lnL = log(static_cast<double>(st.l));
+      const double s = a.reduction == RED_MEAN ? inv_n
+                       : a.reduction == RED_NONE && a.row_scale ? static_cast<double>(a.row_scale[row]) : 1.0;
+      double total = 0.0;
+      if constexpr (LOSS == LOSS_POLICY) {
+        if (lane == 0) {
+          const double lp = (static_cast<double>(s_z[0]) - m) * a.inv_T - lnL;
+          const double H = lnL - static_cast<double>(st.t) / static_cast<double>(st.l) * LN2;
+          const PolicyRow p = policy_row(a.pol, row, lp);
+          total = p.loss;
+          double a0 = -p.dlogp, a1 = 0.0;
+          if (a.ent_coef != 0.0) {
+            total -= a.ent_coef * H;
+            a0 += a.ent_coef * (H - lnL);
+            a1 = a.ent_coef * LN2;
+          }
+          const double f = s * a.inv_T;
+          s_c[0] = static_cast<float>(-p.dlogp * f);
+          coef.m = st.m;
+          coef.a = static_cast<float>(a0 * f / static_cast<double>(st.l));
+          coef.b = static_cast<float>(a1 * f / static_cast<double>(st.l));
+          a.out_logp[row] = static_cast<float>(lp);
+          a.out_entropy[row] = static_cast<float>(H);
+          a.out_kl[row] = static_cast<float>(p.kl);
+        }
+      } else {
+        const TeacherShift ts = teacher_shift(s_u, a.K, lane, a.inv_T, a.teacher_lse, row);
+        double Q = 0.0, kl = 0.0;
+        if (ts.any) {
+          for (int k = lane; k < a.K; k += 32) {
+            const double lq = static_cast<double>(s_u[k]) * a.inv_T - ts.shift;
+            const float q = expf(static_cast<float>(lq));
+            s_c[k] = static_cast<float>(static_cast<double>(q) * a.kd * a.inv_T * s);
+            Q += q;
+            if (!(q == 0.f)) kl += static_cast<double>(q) * (lq - ((static_cast<double>(s_z[k]) - m) * a.inv_T - lnL));
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            Q += __shfl_xor_sync(0xffffffffu, Q, o);
+            kl += __shfl_xor_sync(0xffffffffu, kl, o);
+          }
+        } else {
+          for (int k = lane; k < a.K; k += 32) s_c[k] = 0.f;
+        }
+        if (lane == 0) {
+          if (a.kd != 0.0) total = a.kd * kl;
+          double da = a.kd * Q * a.inv_T, db = 0.0;
+          if (a.ce != 0.0) {
+            const double ln1 = LOSS == LOSS_DISTILL2 ? log(static_cast<double>(st.t)) : lnL;
+            total += a.ce * (m - static_cast<double>(s_z[a.K]) + ln1);
+            if constexpr (LOSS == LOSS_DISTILL2)
+              db = a.ce / static_cast<double>(st.t);
+            else
+              da += a.ce;
+          }
+          s_c[a.K] = static_cast<float>(a.ce * s);
+          coef.m = st.m;
+          coef.a = static_cast<float>(da * s / static_cast<double>(st.l));
+          coef.b = static_cast<float>(db * s);
+          if (a.out_rows) a.out_rows[row] = static_cast<float>(total);
+        }
+      }
+      if (lane == 0) a.row_acc[row] = a.reduction == RED_MEAN ? total : total * s;
+    }
+    __syncthreads();
+    if (g) {
+      const RowCoef c = coef;
+      auto dense = [&](float zj) {
+        const float d = (zj - c.m) * a.zs, e = ex2_approx(d);
+        if constexpr (LOSS == LOSS_POLICY) return e * fmaf(c.b, fmaxf(d, NEG_BIG), c.a);
+        if constexpr (LOSS == LOSS_DISTILL2) return fmaf(e, c.a, ex2_approx((zj - c.m) * LOG2E) * c.b);
+        return e * c.a;
+      };
+      for (int j = tid; j < a.V; j += LOGIT_THREADS) L::store(g + j, dense(L::load(z + j)));
+      __syncthreads();
+      // the sparse entries; equal ids add up, and each of them writes the same sum
+      for (int k = tid; k < K1; k += LOGIT_THREADS) {
+        const int id = s_id[k];
+        if (id < 0) continue;
+        float c_sum = 0.f;
+        for (int i = 0; i < K1; ++i)
+          if (s_id[i] == id) c_sum += s_c[i];
+        L::store(g + id, dense(s_z[k]) - c_sum);
+      }
+    }
+    __syncthreads();  // the shared row data is reused
+  }
+  // the loss, by the last block to finish
+  if (tid == 0) {
+    __threadfence();
+    is_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!is_last) return;
+  __threadfence();
+  const double t = ordered_sum<LOGIT_THREADS>(a.row_acc, a.N, dsum);
+  if (tid == 0) *a.loss = static_cast<float>(a.reduction == RED_MEAN ? t * inv_n : t);
+}
+
+// ------------------------------------------- distillation through the head --
+
+struct TeacherArgs {
+  const int32_t* ids;     // [N][K], the caller's row order
+  const void* u;
+  int u_dtype, K, N, V, ignore_index;
+  const float* teacher_lse;
+  double inv_T, kd, ce;
+  const int* perm;        // row of the caller behind each row
+  const int32_t* y;       // targets in the rows' order
+  // outputs, in the rows' order
+  int32_t* list_ids;      // [N][K + 1]
+  float* list_c;
+  float* list_z;          // read by flce_list_dot_kernel
+  int* list_count;
+  float* list_dense;
+  double* list_const;
+  double* list_lse;
+  double* list_dot;
+  int* status;
+};
+
+// Each row's entries (the teacher's, and the target when hard labels are mixed
+// in) ascending by id, with the coefficients that the G tiles subtract there,
+// and the row's constants:
+//   L = kd sum q log q + (kd Q + ce) lse - sum_k c_k z_k,  c_k = kd q_k / T + ce [target],
+//   G = s ((kd Q / T + ce) p - c).
+// Entries are ranked by counting (id, position) pairs below their own, so the
+// order is the same on every call; equal ids stay separate entries, which the
+// G tiles subtract one after the other.  One CTA per row.
+constexpr int TEACHER_THREADS = 128;
+__global__ void __launch_bounds__(TEACHER_THREADS) flce_teacher_lists_kernel(const TeacherArgs a) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  const int K1 = a.K + 1;
+  int* s_id = reinterpret_cast<int*>(dyn);
+  float* s_u = reinterpret_cast<float*>(s_id + K1);
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int i = blockIdx.x; i < a.N; i += gridDim.x) {
+    const int y = a.y[i];
+    if (y == a.ignore_index) {
+      if (tid == 0) {
+        a.list_count[i] = 0;
+        a.list_dense[i] = 0.f;
+        a.list_const[i] = a.list_lse[i] = 0.0;
+      }
+      continue;
+    }
+    const size_t src = static_cast<size_t>(a.perm[i]);
+    const size_t out = static_cast<size_t>(i) * K1;
+    for (int k = tid; k < K1; k += TEACHER_THREADS) {
+      int id = 0x7fffffff;
+      float u = -INFINITY;
+      if (k < a.K) {
+        const int t = a.ids[src * a.K + k];
+        if (t >= a.V) raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
+        if (t >= 0 && t < a.V) {
+          id = t;
+          u = load_as_f32(a.u, a.u_dtype, src * a.K + k);
+        }
+      } else if (a.ce != 0.0 && y >= 0 && y < a.V) {
+        id = y;
+      }
+      s_id[k] = id;
+      s_u[k] = u;
+    }
+    __syncthreads();
+    const TeacherShift ts = teacher_shift(s_u, a.K, lane, a.inv_T, a.teacher_lse, src);
+    double Q = 0.0, qlogq = 0.0;
+    int count = 0;
+    if (tid < 32) {
+      for (int k = lane; k < K1; k += 32) {
+        if (s_id[k] != 0x7fffffff) ++count;
+        if (k < a.K && ts.any) {
+          const double lq = static_cast<double>(s_u[k]) * a.inv_T - ts.shift;
+          const float q = expf(static_cast<float>(lq));
+          Q += q;
+          if (!(q == 0.f)) qlogq += static_cast<double>(q) * lq;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        Q += __shfl_xor_sync(0xffffffffu, Q, o);
+        qlogq += __shfl_xor_sync(0xffffffffu, qlogq, o);
+        count += __shfl_xor_sync(0xffffffffu, count, o);
+      }
+      if (lane == 0) {
+        a.list_count[i] = count;
+        a.list_dense[i] = static_cast<float>(a.kd * Q * a.inv_T + a.ce);
+        a.list_const[i] = a.kd * qlogq;
+        a.list_lse[i] = a.kd * Q + a.ce;
+      }
+    }
+    for (int k = tid; k < K1; k += TEACHER_THREADS) {
+      const int id = s_id[k];
+      if (id == 0x7fffffff) continue;
+      int rank = 0;
+      for (int j = 0; j < K1; ++j) rank += s_id[j] < id || (s_id[j] == id && j < k) ? 1 : 0;
+      double c = a.ce;
+      if (k < a.K) c = ts.any ? static_cast<double>(expf(static_cast<float>(static_cast<double>(s_u[k]) * a.inv_T - ts.shift))) * a.kd * a.inv_T : 0.0;
+      a.list_ids[out + rank] = id;
+      a.list_c[out + rank] = static_cast<float>(c);
+    }
+    __syncthreads();
+  }
+}
+
+// sum_k c_k z_k of each row, in fp64 (one warp per row, fixed order).
+__global__ void __launch_bounds__(256) flce_list_dot_kernel(const TeacherArgs a) {
+  const int lane = threadIdx.x & 31;
+  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < a.N; i += gridDim.x * 8) {
+    const size_t at = static_cast<size_t>(i) * (a.K + 1);
+    const int n = a.list_count[i];
+    double s = 0.0;
+    for (int k = lane; k < n; k += 32) {
+      const float c = a.list_c[at + k];
+      if (!(c == 0.f)) s += static_cast<double>(c) * static_cast<double>(a.list_z[at + k]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) a.list_dot[i] = s;
+  }
+}
+
+}  // namespace flce

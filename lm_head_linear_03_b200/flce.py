@@ -52,6 +52,12 @@ EXPORTED = (
     "flce_count_valid",
     "flce_pairwise_logistic",
     "flce_forward_backward_sections",
+    "flce_clipped_policy",
+    "flce_policy_loss",
+    "flce_distill_topk",
+    "flce_policy_forward_backward",
+    "flce_distill_workspace_size",
+    "flce_distill_forward_backward",
 )
 REDUCTIONS = {"mean": 0, "sum": 1, "none": 2}
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -148,6 +154,24 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.flce_pairwise_logistic.argtypes = [vp, vp, i64, i32, vp, i32, vp, vp, i32, ctypes.c_double, vp, vp, vp, vp,
                                            vp, vp, vp]
     lib.flce_pairwise_logistic.restype = ctypes.c_int
+    dbl = ctypes.c_double
+    lib.flce_clipped_policy.argtypes = [vp, vp, i64, i32, vp, vp, vp, dbl, dbl, dbl, i32, vp, vp, vp, vp, vp, vp, vp, sz,
+                                        vp]
+    lib.flce_clipped_policy.restype = ctypes.c_int
+    lib.flce_policy_loss.argtypes = [vp, i32, i64, vp, i64, i64, i32, dbl, vp, vp, vp, dbl, dbl, dbl, dbl, i32, vp, vp,
+                                     vp, vp, vp, vp, vp, i64, vp, sz, vp]
+    lib.flce_policy_loss.restype = ctypes.c_int
+    lib.flce_distill_topk.argtypes = [vp, i32, i64, vp, i64, i64, i32, vp, vp, i32, i32, vp, dbl, dbl, dbl, i32, vp, vp,
+                                      vp, vp, vp, i64, vp, sz, vp]
+    lib.flce_distill_topk.restype = ctypes.c_int
+    lib.flce_policy_forward_backward.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, vp, vp, dbl, dbl, dbl, i32, vp, vp,
+                                                 vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_policy_forward_backward.restype = ctypes.c_int
+    lib.flce_distill_workspace_size.argtypes = [i64, i64, i32, i32]
+    lib.flce_distill_workspace_size.restype = sz
+    lib.flce_distill_forward_backward.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, vp, i32, i32, vp, dbl, dbl, dbl,
+                                                  i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_distill_forward_backward.restype = ctypes.c_int
     _lib = lib
     return lib
 

@@ -25,7 +25,9 @@ cross-entropy" pipeline, only without keeping the logit tensor:
   "Installation and the one-line patch": the fused-linear post-training losses
   (ORPO, DPO, ...) take the LM-head weight, the hidden states and the targets
   and return the loss; :func:`pairwise_logistic` is the DPO-form loss on the
-  per-sequence log-probabilities that the head's row losses give.
+  per-sequence log-probabilities that the head's row losses give;
+  :func:`policy_reference` and :func:`distill_reference` are a clipped policy
+  loss and a top-logit distillation on a logit matrix.
 
 The oracle therefore *does* materialise the logits (that is the plain
 definition) and follows these steps, with ``n`` the number of non-ignored rows:
@@ -353,3 +355,110 @@ def pairwise_logistic(row_loss, y, seq_start, chosen, rejected, beta: float, ref
         w[st[s]:st[s + 1]] = -grad[s]
     w[y == ignore_index] = 0.0
     return loss, logp, grad, w
+
+
+# ---------------------------------------------------------------------------
+# Post-training losses of the output layer: clipped policy loss with a KL term,
+# distillation from a teacher's top logits.
+# ---------------------------------------------------------------------------
+
+def clipped_policy(logp, valid, old_logp, advantages, ref_logp=None, clip_low: float = 0.2, clip_high: float = 0.2,
+                   kl_coef: float = 0.0):
+    """Per row with log-probability ``lp``: ``r = exp(lp - old)`` (1 when
+    ``old_logp`` is None), ``kl = exp(ref - lp) - (ref - lp) - 1`` (0 without a
+    reference) and ``L = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) +
+    kl_coef kl``.  Returns ``(L, dL/dlp, kl)``, 0 where ``valid`` is false.  A
+    ratio on a border counts as not clipped."""
+    valid = np.asarray(valid, dtype=bool)
+    lp = np.where(valid, _f64(logp), 0.0)
+    A = np.where(valid, _f64(advantages), 0.0)
+    r = np.ones_like(lp) if old_logp is None else np.exp(lp - np.where(valid, _f64(old_logp), 0.0))
+    rc = np.clip(r, 1.0 - clip_low, 1.0 + clip_high)
+    L = -np.minimum(r * A, rc * A)
+    clipped = np.where(A >= 0, r > 1.0 + clip_high, r < 1.0 - clip_low)
+    dL = np.where(clipped, 0.0, -A * r)
+    kl = np.zeros_like(lp)
+    if ref_logp is not None:
+        d = np.where(valid, _f64(ref_logp), 0.0) - lp
+        kl = np.expm1(d) - d
+        L = L + kl_coef * kl
+        dL = dL - kl_coef * np.expm1(d)
+    zero = np.zeros_like(lp)
+    return np.where(valid, L, zero), np.where(valid, dL, zero), np.where(valid, kl, zero)
+
+
+def _softmax_rows(Z):
+    """(log-softmax, softmax) of each row; entries of -infinity have probability 0."""
+    m = Z.max(axis=1, keepdims=True)
+    e = np.exp(Z - m)
+    l = e.sum(axis=1, keepdims=True)
+    return Z - m - np.log(l), e / l
+
+
+def policy_reference(Z, y, old_logp, advantages, ref_logp=None, clip_low: float = 0.2, clip_high: float = 0.2,
+                     kl_coef: float = 0.0, entropy_coef: float = 0.0, temperature: float = 1.0,
+                     ignore_index: int = IGNORE_INDEX, reduction: str = "mean", grad_row_scale=None):
+    """The clipped policy loss on logits Z[N,V] of softmax(Z / temperature), with
+    ``- entropy_coef * H``.  Returns ``(loss, dZ, logp, H, kl)``."""
+    Z = _f64(Z)
+    y = _i64(y)
+    N, V = Z.shape
+    valid = valid_mask(y, V, ignore_index)
+    rows = np.arange(N)
+    yv = np.where(valid, y, 0)
+    s = row_scale(valid, reduction, grad_row_scale)
+    Z = np.where(valid[:, None], Z, 0.0) / temperature
+    logp_all, P = _softmax_rows(Z)
+    lp = logp_all[rows, yv]
+    plogp = np.where(P > 0, P * np.where(P > 0, logp_all, 0.0), 0.0)
+    H = -plogp.sum(axis=1)
+    L, dL, kl = clipped_policy(lp, valid, old_logp, advantages, ref_logp, clip_low, clip_high, kl_coef)
+    loss = float((s * np.where(valid, L - entropy_coef * H, 0.0)).sum())
+    G = -dL[:, None] * P
+    G[rows, yv] += dL
+    G += entropy_coef * (plogp + P * H[:, None])
+    G *= (s * valid / temperature)[:, None]
+    return loss, G, np.where(valid, lp, 0.0), np.where(valid, H, 0.0), kl
+
+
+def distill_reference(Z, y, teacher_ids, teacher_logits, teacher_lse=None, temperature: float = 1.0,
+                      kd_weight: float = 1.0, ce_weight: float = 0.0, ignore_index: int = IGNORE_INDEX,
+                      reduction: str = "mean", grad_row_scale=None):
+    """Distillation on logits Z[N,V] from K teacher logits per row (negative id:
+    no entry): ``q = softmax(u / T)`` over the row's entries, or ``exp(u / T -
+    teacher_lse)``; ``L = kd sum q (log q - log p) + ce (lse(z) - z_y)`` with
+    ``p = softmax(z / T)``.  Returns ``(loss, dZ, row_loss)``."""
+    Z = _f64(Z)
+    y = _i64(y)
+    N, V = Z.shape
+    ids = _i64(teacher_ids)
+    T = float(temperature)
+    valid = valid_mask(y, V, ignore_index)
+    s = row_scale(valid, reduction, grad_row_scale)
+    Z = np.where(valid[:, None], Z, 0.0)
+    u = np.where(valid[:, None] & (ids >= 0), _f64(teacher_logits) / T, -np.inf)
+    logp, P = _softmax_rows(Z / T)
+    L = np.zeros(N)
+    G = np.zeros_like(Z)
+    for i in range(N):
+        if not valid[i]:
+            continue
+        k = np.nonzero(u[i] > -np.inf)[0]
+        if len(k):
+            if teacher_lse is None:
+                top = u[i, k].max()
+                logq = u[i, k] - top - np.log(np.exp(u[i, k] - top).sum())
+            else:
+                logq = u[i, k] - float(_f64(teacher_lse)[i])
+            q = np.exp(logq)
+            L[i] += kd_weight * (q * (logq - logp[i, ids[i, k]])).sum()
+            G[i] += kd_weight / T * q.sum() * P[i]
+            np.subtract.at(G[i], ids[i, k], kd_weight / T * q)
+    if ce_weight:
+        logp1, P1 = _softmax_rows(Z)
+        rows = np.arange(N)
+        yv = np.where(valid, y, 0)
+        L += ce_weight * np.where(valid, -logp1[rows, yv], 0.0)
+        G += ce_weight * P1 * valid[:, None]
+        G[rows, yv] -= ce_weight * valid
+    return float((s * L).sum()), G * s[:, None], L
