@@ -876,15 +876,48 @@ flce_status_t begin_rows(const int32_t* y, int64_t N, int32_t ignore_index, uint
   return cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
 }
 
+// How a row of `V` elements is laid over a cluster (see the kernel).
+struct LogitShape {
+  int cluster, threads, nch;
+};
+LogitShape logit_shape(int64_t N, int64_t V, int es, int num_sms) {
+  const int64_t chunks = V * es / 16 + 1;
+  int cs = 1;
+  while (cs < LOGIT_MAX_CLUSTER && (chunks > cs * 2048 || (N * cs * 2 <= num_sms && chunks > cs * 512))) cs *= 2;
+  const int64_t per = (chunks + cs - 1) / cs;
+  return {cs, per > 2048 ? 512 : 256, per > 512 ? 8 : 2};
+}
+
+template <typename T, int LOSS, int THREADS, int NCH>
+cudaError_t launch_logit_shape(const LogitArgs& a, int cs, size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.N, 1 << 20) * cs), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(cs);
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, flce_logit_loss_kernel<T, LOSS, THREADS, NCH>, a);
+}
+
+template <typename T, int LOSS>
+cudaError_t launch_logit_type(const LogitArgs& a, int num_sms, size_t smem, cudaStream_t stream) {
+  const LogitShape h = logit_shape(a.N, a.V, sizeof(T), num_sms);
+  if (h.threads == 512) return launch_logit_shape<T, LOSS, 512, 8>(a, h.cluster, smem, stream);
+  if (h.nch == 8) return launch_logit_shape<T, LOSS, 256, 8>(a, h.cluster, smem, stream);
+  return launch_logit_shape<T, LOSS, 256, 2>(a, h.cluster, smem, stream);
+}
+
 template <int LOSS>
-void launch_logit_loss(const LogitArgs& a, int dtype, int num_sms, size_t smem, cudaStream_t stream) {
-  const int grid = static_cast<int>(std::min<int64_t>(a.N, static_cast<int64_t>(num_sms) * 256));
-  if (dtype == FLCE_DTYPE_BF16)
-    flce_logit_loss_kernel<__nv_bfloat16, LOSS><<<grid, LOGIT_THREADS, smem, stream>>>(a);
-  else if (dtype == FLCE_DTYPE_FP16)
-    flce_logit_loss_kernel<__half, LOSS><<<grid, LOGIT_THREADS, smem, stream>>>(a);
-  else
-    flce_logit_loss_kernel<float, LOSS><<<grid, LOGIT_THREADS, smem, stream>>>(a);
+cudaError_t launch_logit_loss(const LogitArgs& a, int dtype, int num_sms, size_t smem, cudaStream_t stream) {
+  if (dtype == FLCE_DTYPE_BF16) return launch_logit_type<__nv_bfloat16, LOSS>(a, num_sms, smem, stream);
+  if (dtype == FLCE_DTYPE_FP16) return launch_logit_type<__half, LOSS>(a, num_sms, smem, stream);
+  return launch_logit_type<float, LOSS>(a, num_sms, smem, stream);
 }
 
 // What the two losses on logits share: device check, counters, launch.
@@ -902,14 +935,11 @@ flce_status_t enqueue_logit_loss(LogitArgs& a, int loss, int32_t dtype, uint8_t*
   const size_t smem = 16 * (loss == LOSS_POLICY ? 1 : static_cast<size_t>(a.K) + 1);
   size_t slot;
   prof_begin(stream, KIND_LOGIT_LOSS, &slot);
-  if (loss == LOSS_POLICY)
-    launch_logit_loss<LOSS_POLICY>(a, dtype, di.num_sms, smem, stream);
-  else if (loss == LOSS_DISTILL)
-    launch_logit_loss<LOSS_DISTILL>(a, dtype, di.num_sms, smem, stream);
-  else
-    launch_logit_loss<LOSS_DISTILL2>(a, dtype, di.num_sms, smem, stream);
+  const cudaError_t e = loss == LOSS_POLICY    ? launch_logit_loss<LOSS_POLICY>(a, dtype, di.num_sms, smem, stream)
+                        : loss == LOSS_DISTILL ? launch_logit_loss<LOSS_DISTILL>(a, dtype, di.num_sms, smem, stream)
+                                               : launch_logit_loss<LOSS_DISTILL2>(a, dtype, di.num_sms, smem, stream);
   prof_end(stream, slot);
-  return cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
 }
 
 }  // namespace

@@ -39,18 +39,55 @@ template <typename T>
 struct LogitTraits;
 template <>
 struct LogitTraits<__nv_bfloat16> {
+  static constexpr int EPC = 8;  // elements of a 16-byte chunk
+  static constexpr uint32_t NEG_INF = 0xff80ff80u;
   __device__ static float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-  __device__ static void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+  __device__ static __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
+  __device__ static void unpack(const uint4& v, float (&f)[8]) { unpack_bf16x8(v, f); }
+  __device__ static uint4 pack(const float (&o)[8]) {
+    return make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+  }
 };
 template <>
 struct LogitTraits<__half> {
+  static constexpr int EPC = 8;
+  static constexpr uint32_t NEG_INF = 0xfc00fc00u;
   __device__ static float load(const __half* p) { return __half2float(*p); }
-  __device__ static void store(__half* p, float v) { *p = __float2half_rn(v); }
+  __device__ static __half round(float v) { return __float2half_rn(v); }
+  __device__ static void unpack(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+      f[2 * e] = t.x;
+      f[2 * e + 1] = t.y;
+    }
+  }
+  __device__ static uint4 pack(const float (&o)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 h = __floats2half2_rn(o[2 * e], o[2 * e + 1]);
+      w[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
 template <>
 struct LogitTraits<float> {
+  static constexpr int EPC = 4;
+  static constexpr uint32_t NEG_INF = 0xff800000u;
   __device__ static float load(const float* p) { return *p; }
-  __device__ static void store(float* p, float v) { *p = v; }
+  __device__ static float round(float v) { return v; }
+  __device__ static void unpack(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+  }
+  __device__ static uint4 pack(const float (&o)[4]) {
+    return make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3]));
+  }
 };
 
 enum : int { DT_BF16 = 0, DT_FP16 = 1, DT_FP32 = 2 };
@@ -264,39 +301,77 @@ __device__ __forceinline__ void stat_merge(RowStat& s, const RowStat& o, float z
   s.m = m;
 }
 
-constexpr int LOGIT_THREADS = 512;
-
 // What the gradient pass needs of a row.
 struct RowCoef {
-  float m;       // the row's maximum
   float a, b;    // dense part: e (a + b arg), or a e + b e1 with two softmaxes
 };
 
-// One CTA per row: an online pass over the row, the row's scalars, a second
-// pass that writes the gradient, then the sparse entries.
-template <typename T, int LOSS>
-__global__ void __launch_bounds__(LOGIT_THREADS) flce_logit_loss_kernel(const LogitArgs a) {
+constexpr int LOGIT_MAX_CLUSTER = 8;
+
+// A row is split over the CTAs of a cluster, each of which holds its part in
+// registers: 16-byte chunks on 16-byte boundaries, NCH per thread, so the
+// logits are read from memory once and all of a thread's loads are in flight
+// together.  (What lies beyond the registers, in rows longer than
+// cluster * THREADS * NCH chunks, is read a second time for the gradient.)
+// The up to 2 * (EPC - 1) elements in front of the first and behind the last
+// boundary are held one per thread by the cluster's first CTA.
+//
+// Statistics: each warp folds its elements under its own maximum and writes one
+// record into every CTA of the cluster; after one cluster barrier every warp
+// merges all records in a fixed order, so all CTAs know the row's totals
+// without a second exchange.  Warp 0 turns them into the row's outputs (first
+// CTA) and the gradient's coefficients; then each CTA writes its part of the
+// gradient and, behind a CTA barrier, the sparse entries that lie in it.
+template <typename T, int LOSS, int THREADS, int NCH>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kernel(const LogitArgs a) {
   using L = LogitTraits<T>;
+  constexpr int EPC = L::EPC;
+  constexpr int WARPS = THREADS / 32;
   extern __shared__ __align__(16) uint8_t dyn[];
   const int K1 = LOSS == LOSS_POLICY ? 1 : a.K + 1;
   int* s_id = reinterpret_cast<int*>(dyn);           // sparse entries' vocabulary ids (-1: none)
   float* s_u = reinterpret_cast<float*>(s_id + K1);  // teacher logits
   float* s_c = s_u + K1;                             // coefficient subtracted at the entry
   float* s_z = s_c + K1;                             // the student's logit there
-  __shared__ RowStat w_stat[LOGIT_THREADS / 32];
+  __shared__ float4 rec[2][LOGIT_MAX_CLUSTER * WARPS];
   __shared__ RowCoef coef;
-  __shared__ double dsum[LOGIT_THREADS / 32];
+  __shared__ double dsum[WARPS];
   __shared__ bool is_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cs = static_cast<int>(cluster_nctarank());
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int clusters = gridDim.x / cs;
   const int n_valid = *a.n_valid;
   const double inv_n = n_valid > 0 ? 1.0 / static_cast<double>(n_valid) : 0.0;
-  for (int row = blockIdx.x; row < a.N; row += gridDim.x) {
+  const uint64_t once = l2_evict_first();
+  int parity = 0;
+  for (int row = blockIdx.x / cs; row < a.N; row += clusters) {
     const T* z = static_cast<const T*>(a.z) + static_cast<long long>(row) * a.ld;
     T* g = a.g ? static_cast<T*>(a.g) + static_cast<long long>(row) * a.ldg : nullptr;
+    // elements in front of the first 16-byte boundary, chunks, elements behind the last one
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
+    const int head = min(a.V, mis ? EPC - mis : 0);
+    const int chunks = (a.V - head) / EPC;
+    const int edges = a.V - chunks * EPC;
+    const int per = (chunks + cs - 1) / cs;
+    const int c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
+    const T* zc = z + head;
+    // the gradient row shares the logits' alignment, or its elements are stored one by one
+    const bool vec_out = g && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+    const int edge_col = rank == 0 && tid < edges ? (tid < head ? tid : a.V - edges + tid) : -1;
+    auto put = [&](int c, const float (&o)[EPC]) {
+      if (vec_out) {
+        st_l2hint_v4(reinterpret_cast<uint4*>(g + head) + c, L::pack(o), once);
+      } else {
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) g[head + c * EPC + e] = L::round(o[e]);
+      }
+    };
+
     const int y = a.y[row];
     const bool in_range = y >= 0 && y < a.V;
     if (y == a.ignore_index || !in_range) {
-      if (tid == 0) {
+      if (rank == 0 && tid == 0) {
         if (y != a.ignore_index) raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
         a.row_acc[row] = 0.0;
         if constexpr (LOSS == LOSS_POLICY) {
@@ -305,12 +380,25 @@ __global__ void __launch_bounds__(LOGIT_THREADS) flce_logit_loss_kernel(const Lo
           a.out_rows[row] = 0.f;
         }
       }
-      if (g)
-        for (int j = tid; j < a.V; j += LOGIT_THREADS) L::store(g + j, 0.f);
+      if (g) {
+        const float zero[EPC] = {};
+        for (int c = c0 + tid; c < c1; c += THREADS) put(c, zero);
+        if (edge_col >= 0) g[edge_col] = L::round(0.f);
+      }
       continue;
     }
+
+    // ---- the row's part of this CTA
+    uint4 raw[NCH];
+#pragma unroll
+    for (int u = 0; u < NCH; ++u) {
+      const int c = c0 + u * THREADS + tid;
+      raw[u] = c < c1 ? ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + c, once)
+                      : make_uint4(L::NEG_INF, L::NEG_INF, L::NEG_INF, L::NEG_INF);
+    }
+    const float edge = edge_col >= 0 ? L::load(z + edge_col) : -INFINITY;
     // the sparse entries: the teacher's, then the target
-    for (int k = tid; k < K1; k += LOGIT_THREADS) {
+    for (int k = tid; k < K1; k += THREADS) {
       int id = y;
       float u = -INFINITY;
       if (k < K1 - 1) {
@@ -326,32 +414,85 @@ __global__ void __launch_bounds__(LOGIT_THREADS) flce_logit_loss_kernel(const Lo
       s_u[k] = u;
       s_z[k] = id < 0 ? 0.f : L::load(z + id);
     }
+
+    // ---- statistics
     RowStat st{-FLT_MAX, 0.f, 0.f};
-    for (int j = tid; j < a.V; j += LOGIT_THREADS) stat_add<LOSS>(st, L::load(z + j), a.zs);
+    for (int c = c0 + NCH * THREADS + tid; c < c1; c += THREADS) {  // beyond the registers
+      float f[EPC];
+      L::unpack(ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + c, l2_evict_normal()), f);
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) stat_add<LOSS>(st, f[e], a.zs);
+    }
+    RowStat w{fmaxf(st.m, edge), 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < NCH; ++u) {
+      float f[EPC];
+      L::unpack(raw[u], f);
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) w.m = fmaxf(w.m, f[e]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) w.m = fmaxf(w.m, __shfl_xor_sync(0xffffffffu, w.m, o));
+    auto fold = [&](float x) {
+      const float d = (x - w.m) * a.zs, e = ex2_approx(d);
+      w.l += e;
+      if constexpr (LOSS == LOSS_POLICY) w.t = fmaf(e, fmaxf(d, NEG_BIG), w.t);
+      if constexpr (LOSS == LOSS_DISTILL2) w.t += ex2_approx((x - w.m) * LOG2E);
+    };
+#pragma unroll
+    for (int u = 0; u < NCH; ++u) {
+      float f[EPC];
+      L::unpack(raw[u], f);
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) fold(f[e]);
+    }
+    fold(edge);
+    if (c1 - c0 > NCH * THREADS) stat_merge<LOSS>(w, st, a.zs);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      RowStat other;
-      other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-      other.l = __shfl_xor_sync(0xffffffffu, st.l, o);
-      other.t = __shfl_xor_sync(0xffffffffu, st.t, o);
-      stat_merge<LOSS>(st, other, a.zs);
+      w.l += __shfl_xor_sync(0xffffffffu, w.l, o);
+      w.t += __shfl_xor_sync(0xffffffffu, w.t, o);
     }
-    if (lane == 0) w_stat[warp] = st;
-    __syncthreads();
+    if (cs == 1) {
+      if (lane == 0) rec[parity][warp] = make_float4(w.m, w.l, w.t, 0.f);
+      __syncthreads();
+    } else {
+      if (lane < cs)
+        st_cluster_f4(mapa_shared(smem_u32(&rec[parity][rank * WARPS + warp]), lane), make_float4(w.m, w.l, w.t, 0.f));
+      cluster_sync_all();
+    }
+
+    // ---- the row's totals (every warp, the same order everywhere)
+    const int records = cs * WARPS;
+    w.m = -FLT_MAX;
+    for (int r = lane; r < records; r += 32) w.m = fmaxf(w.m, rec[parity][r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) w.m = fmaxf(w.m, __shfl_xor_sync(0xffffffffu, w.m, o));
     if (warp == 0) {
-      st = w_stat[0];
-      for (int w = 1; w < LOGIT_THREADS / 32; ++w) stat_merge<LOSS>(st, w_stat[w], a.zs);
+      w.l = w.t = 0.f;
+      for (int r = lane; r < records; r += 32) {
+        const float4 v = rec[parity][r];
+        RowStat o{w.m, 0.f, 0.f};
+        stat_merge<LOSS>(o, RowStat{v.x, v.y, v.z}, a.zs);
+        w.l += o.l;
+        w.t += o.t;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        w.l += __shfl_xor_sync(0xffffffffu, w.l, o);
+        w.t += __shfl_xor_sync(0xffffffffu, w.t, o);
+      }
       // Log-probabilities as (z - m)/T - ln L: the difference first, so that a
       // row whose every logit is the type's lowest value still has one.
-      const double m = static_cast<double>(st.m);
-      const double lnL = log(static_cast<double>(st.l));
+      const double m = static_cast<double>(w.m);
+      const double lnL = log(static_cast<double>(w.l));
       const double s = a.reduction == RED_MEAN ? inv_n
                        : a.reduction == RED_NONE && a.row_scale ? static_cast<double>(a.row_scale[row]) : 1.0;
       double total = 0.0;
       if constexpr (LOSS == LOSS_POLICY) {
         if (lane == 0) {
           const double lp = (static_cast<double>(s_z[0]) - m) * a.inv_T - lnL;
-          const double H = lnL - static_cast<double>(st.t) / static_cast<double>(st.l) * LN2;
+          const double H = lnL - static_cast<double>(w.t) / static_cast<double>(w.l) * LN2;
           const PolicyRow p = policy_row(a.pol, row, lp);
           total = p.loss;
           double a0 = -p.dlogp, a1 = 0.0;
@@ -362,12 +503,13 @@ __global__ void __launch_bounds__(LOGIT_THREADS) flce_logit_loss_kernel(const Lo
           }
           const double f = s * a.inv_T;
           s_c[0] = static_cast<float>(-p.dlogp * f);
-          coef.m = st.m;
-          coef.a = static_cast<float>(a0 * f / static_cast<double>(st.l));
-          coef.b = static_cast<float>(a1 * f / static_cast<double>(st.l));
-          a.out_logp[row] = static_cast<float>(lp);
-          a.out_entropy[row] = static_cast<float>(H);
-          a.out_kl[row] = static_cast<float>(p.kl);
+          coef.a = static_cast<float>(a0 * f / static_cast<double>(w.l));
+          coef.b = static_cast<float>(a1 * f / static_cast<double>(w.l));
+          if (rank == 0) {
+            a.out_logp[row] = static_cast<float>(lp);
+            a.out_entropy[row] = static_cast<float>(H);
+            a.out_kl[row] = static_cast<float>(p.kl);
+          }
         }
       } else {
         const TeacherShift ts = teacher_shift(s_u, a.K, lane, a.inv_T, a.teacher_lse, row);
@@ -392,54 +534,79 @@ __global__ void __launch_bounds__(LOGIT_THREADS) flce_logit_loss_kernel(const Lo
           if (a.kd != 0.0) total = a.kd * kl;
           double da = a.kd * Q * a.inv_T, db = 0.0;
           if (a.ce != 0.0) {
-            const double ln1 = LOSS == LOSS_DISTILL2 ? log(static_cast<double>(st.t)) : lnL;
+            const double ln1 = LOSS == LOSS_DISTILL2 ? log(static_cast<double>(w.t)) : lnL;
             total += a.ce * (m - static_cast<double>(s_z[a.K]) + ln1);
             if constexpr (LOSS == LOSS_DISTILL2)
-              db = a.ce / static_cast<double>(st.t);
+              db = a.ce / static_cast<double>(w.t);
             else
               da += a.ce;
           }
           s_c[a.K] = static_cast<float>(a.ce * s);
-          coef.m = st.m;
-          coef.a = static_cast<float>(da * s / static_cast<double>(st.l));
+          coef.a = static_cast<float>(da * s / static_cast<double>(w.l));
           coef.b = static_cast<float>(db * s);
-          if (a.out_rows) a.out_rows[row] = static_cast<float>(total);
+          if (rank == 0 && a.out_rows) a.out_rows[row] = static_cast<float>(total);
         }
       }
-      if (lane == 0) a.row_acc[row] = a.reduction == RED_MEAN ? total : total * s;
+      if (rank == 0 && lane == 0) a.row_acc[row] = a.reduction == RED_MEAN ? total : total * s;
     }
     __syncthreads();
+
+    // ---- the gradient
     if (g) {
       const RowCoef c = coef;
-      auto dense = [&](float zj) {
-        const float d = (zj - c.m) * a.zs, e = ex2_approx(d);
+      const float m = w.m;
+      auto dense = [&](float x) {
+        const float d = (x - m) * a.zs, e = ex2_approx(d);
         if constexpr (LOSS == LOSS_POLICY) return e * fmaf(c.b, fmaxf(d, NEG_BIG), c.a);
-        if constexpr (LOSS == LOSS_DISTILL2) return fmaf(e, c.a, ex2_approx((zj - c.m) * LOG2E) * c.b);
+        if constexpr (LOSS == LOSS_DISTILL2) return fmaf(e, c.a, ex2_approx((x - m) * LOG2E) * c.b);
         return e * c.a;
       };
-      for (int j = tid; j < a.V; j += LOGIT_THREADS) L::store(g + j, dense(L::load(z + j)));
+#pragma unroll
+      for (int u = 0; u < NCH; ++u) {
+        const int ch = c0 + u * THREADS + tid;
+        if (ch < c1) {
+          float f[EPC];
+          L::unpack(raw[u], f);
+#pragma unroll
+          for (int e = 0; e < EPC; ++e) f[e] = dense(f[e]);
+          put(ch, f);
+        }
+      }
+      for (int ch = c0 + NCH * THREADS + tid; ch < c1; ch += THREADS) {
+        float f[EPC];
+        L::unpack(ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + ch, once), f);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) f[e] = dense(f[e]);
+        put(ch, f);
+      }
+      if (edge_col >= 0) g[edge_col] = L::round(dense(edge));
       __syncthreads();
-      // the sparse entries; equal ids add up, and each of them writes the same sum
-      for (int k = tid; k < K1; k += LOGIT_THREADS) {
+      // The sparse entries of this CTA's part; equal ids add up, and each of
+      // them writes the same sum.
+      const int lo = head + c0 * EPC, hi = head + c1 * EPC;
+      for (int k = tid; k < K1; k += THREADS) {
         const int id = s_id[k];
-        if (id < 0) continue;
+        const bool mine = id >= lo && id < hi ? true : rank == 0 && id >= 0 && (id < head || id >= head + chunks * EPC);
+        if (!mine) continue;
         float c_sum = 0.f;
         for (int i = 0; i < K1; ++i)
           if (s_id[i] == id) c_sum += s_c[i];
-        L::store(g + id, dense(s_z[k]) - c_sum);
+        g[id] = L::round(dense(s_z[k]) - c_sum);
       }
     }
     __syncthreads();  // the shared row data is reused
+    parity ^= 1;
   }
-  // the loss, by the last block to finish
+  // the loss, by the last cluster to finish
+  if (rank != 0) return;
   if (tid == 0) {
     __threadfence();
-    is_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    is_last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(clusters - 1);
   }
   __syncthreads();
   if (!is_last) return;
   __threadfence();
-  const double t = ordered_sum<LOGIT_THREADS>(a.row_acc, a.N, dsum);
+  const double t = ordered_sum<THREADS>(a.row_acc, a.N, dsum);
   if (tid == 0) *a.loss = static_cast<float>(a.reduction == RED_MEAN ? t * inv_n : t);
 }
 

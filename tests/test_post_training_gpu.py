@@ -51,18 +51,19 @@ def _close(got, ref, tol, what):
     assert not bad.any(), f"{what}: {int(bad.sum())} values off, e.g. {got[bad][0]} against {ref[bad][0]}"
 
 
-def _padded(Z, pad):
-    """Z on the GPU as rows of a buffer with `pad` more columns of NaN."""
-    if not pad:
+def _padded(Z, pad, lead=0):
+    """Z on the GPU as columns of a buffer with `lead` columns of NaN in front and `pad` behind."""
+    if not pad and not lead:
         return Z.cuda(), None
-    buf = torch.full((Z.shape[0], Z.shape[1] + pad), math.nan, dtype=Z.dtype).cuda()
-    buf[:, : Z.shape[1]] = Z.cuda()
-    return buf[:, : Z.shape[1]], buf
+    buf = torch.full((Z.shape[0], lead + Z.shape[1] + pad), math.nan, dtype=Z.dtype).cuda()
+    view = buf[:, lead:lead + Z.shape[1]]
+    view.copy_(Z)
+    return view, buf
 
 
-def _check_policy(Z, y, old, adv, ref, *, pad=0, kl=0.1, ent=0.0, T=1.0, reduction="mean", scale=None, grad="new"):
+def _check_policy(Z, y, old, adv, ref, *, pad=0, lead=0, kl=0.1, ent=0.0, T=1.0, reduction="mean", scale=None, grad="new"):
     F = _lib()
-    Zd, buf = _padded(Z, pad)
+    Zd, buf = _padded(Z, pad, lead)
     yd, od, ad, rd, sd = _cuda(y, old, adv, ref, scale)
     before = Zd.clone()
     loss, status, lp, H, klo, g = F.policy_loss(Zd, yd, od, ad, ref_logp=rd, clip_low=0.2, clip_high=0.28, kl_coef=kl,
@@ -98,7 +99,7 @@ def _check_policy(Z, y, old, adv, ref, *, pad=0, kl=0.1, ent=0.0, T=1.0, reducti
     tol = tol + np.abs(rG) * (torch.finfo(Z.dtype).eps / 2) + TINY[Z.dtype]
     _close(_np(g), rG, tol, "dlogits")
     if buf is not None:
-        assert torch.isnan(buf[:, V:]).all(), "columns behind the vocabulary were written"
+        assert torch.isnan(buf[:, :lead]).all() and torch.isnan(buf[:, lead + V:]).all(), "columns outside were written"
         if grad == "new":
             assert torch.equal(torch.nan_to_num(Zd), torch.nan_to_num(before))
     return g
@@ -149,20 +150,14 @@ def test_policy_in_place(dtype, pad):
 @pytest.mark.parametrize("dtype", DT, ids=["bf16", "fp16", "fp32"])
 def test_policy_unaligned_views(dtype):
     """Rows that start anywhere: a slice of columns of a wider buffer, with a
-    gradient whose rows are aligned otherwise."""
-    F = _lib()
+    gradient whose rows are aligned otherwise, and in place.  Where a row starts
+    decides which elements share a partial sum, so the views agree with the
+    oracle, not bit by bit with one another."""
     Z, y, old, adv, ref = policy_case(6, 1234, seed=8, dtype=dtype)
-    want = _check_policy(Z, y, old, adv, ref)
-    yd, od, ad, rd = _cuda(y, old, adv, ref)
     for lead in range(1, 9):
-        buf = torch.full((6, 1300 + lead), math.nan, dtype=dtype, device="cuda")
-        view = buf[:, lead:lead + 1234]
-        view.copy_(Z)
-        g = F.policy_loss(view, yd, od, ad, ref_logp=rd, clip_high=0.28, kl_coef=0.1)[-1]
-        assert torch.equal(g, want)
-        F.policy_loss(view, yd, od, ad, ref_logp=rd, clip_high=0.28, kl_coef=0.1, grad="inplace")
-        assert torch.equal(view, want)
-        assert torch.isnan(buf[:, :lead]).all() and torch.isnan(buf[:, lead + 1234:]).all()
+        new = _check_policy(Z, y, old, adv, ref, lead=lead, pad=66)
+        same = _check_policy(Z, y, old, adv, ref, lead=lead, pad=66, grad="inplace")
+        assert torch.equal(new, same)
 
 
 @pytest.mark.parametrize("dtype", DT, ids=["bf16", "fp16", "fp32"])
