@@ -932,12 +932,16 @@ flce_status_t enqueue_logit_loss(LogitArgs& a, int loss, int32_t dtype, uint8_t*
   a.ticket = reinterpret_cast<unsigned int*>(ws + L.ctrl + 4);
   a.n_valid = reinterpret_cast<const int*>(ws + L.ctrl + 8);
   a.row_acc = reinterpret_cast<double*>(ws + L.row_acc);
-  const size_t smem = 16 * (loss == LOSS_POLICY ? 1 : static_cast<size_t>(a.K) + 1);
+  const size_t smem = 16 * (is_policy(loss) ? 1 : static_cast<size_t>(a.K) + 1);
   size_t slot;
   prof_begin(stream, KIND_LOGIT_LOSS, &slot);
-  const cudaError_t e = loss == LOSS_POLICY    ? launch_logit_loss<LOSS_POLICY>(a, dtype, di.num_sms, smem, stream)
-                        : loss == LOSS_DISTILL ? launch_logit_loss<LOSS_DISTILL>(a, dtype, di.num_sms, smem, stream)
-                                               : launch_logit_loss<LOSS_DISTILL2>(a, dtype, di.num_sms, smem, stream);
+  cudaError_t e;
+  switch (loss) {
+    case LOSS_POLICY: e = launch_logit_loss<LOSS_POLICY>(a, dtype, di.num_sms, smem, stream); break;
+    case LOSS_POLICY_ENT: e = launch_logit_loss<LOSS_POLICY_ENT>(a, dtype, di.num_sms, smem, stream); break;
+    case LOSS_DISTILL: e = launch_logit_loss<LOSS_DISTILL>(a, dtype, di.num_sms, smem, stream); break;
+    default: e = launch_logit_loss<LOSS_DISTILL2>(a, dtype, di.num_sms, smem, stream); break;
+  }
   prof_end(stream, slot);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
 }
@@ -1239,7 +1243,7 @@ flce_status_t flce_policy_loss(const void* logits, int32_t dtype, int64_t ld, co
   a.out_logp = d_logp;
   a.out_entropy = d_entropy;
   a.out_kl = d_kl;
-  return enqueue_logit_loss(a, LOSS_POLICY, dtype, static_cast<uint8_t*>(workspace), stream);
+  return enqueue_logit_loss(a, entropy_coef != 0.0 ? LOSS_POLICY_ENT : LOSS_POLICY, dtype, static_cast<uint8_t*>(workspace), stream);
 }
 
 flce_status_t flce_distill_topk(const void* logits, int32_t dtype, int64_t ld, const int32_t* y, int64_t N, int64_t V,

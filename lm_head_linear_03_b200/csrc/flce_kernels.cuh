@@ -1721,7 +1721,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) flce_combine_kernel(const Com
       const int src = a.perm[i];
       a.logp[src] = static_cast<float>(-row);
       if (valid) {
-        const PolicyRow p = policy_row(a.pol, src, -row);
+        const PolicyRow p = policy_row(a.pol, policy_load(a.pol, src), -row);
         li = a.reduction == RED_NONE && a.grad_row_scale ? p.loss * static_cast<double>(a.grad_row_scale[i]) : p.loss;
         a.row_mult[i] = static_cast<float>(-p.dlogp);
       }

@@ -36,17 +36,26 @@ constexpr float NEG_BIG = -1e4f;  // exponents below this are 0 in every format;
 // ------------------------------------------------------- logits by type --
 
 template <typename T>
-struct LogitTraits;
+struct LogitTraits;  // a 16-byte chunk of logits: unpacked in pairs, packed, its maximum
 template <>
 struct LogitTraits<__nv_bfloat16> {
-  static constexpr int EPC = 8;  // elements of a 16-byte chunk
+  static constexpr int EPC = 8;  // elements of a chunk
   static constexpr uint32_t NEG_INF = 0xff80ff80u;
   __device__ static float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   __device__ static __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
-  __device__ static void unpack(const uint4& v, float (&f)[8]) { unpack_bf16x8(v, f); }
-  __device__ static uint4 pack(const float (&o)[8]) {
-    return make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+  __device__ static uint64_t pair(const uint4& v, int i) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(&v)[i];
+    return f32x2(bf16lo_to_f32(w), bf16hi_to_f32(w));
   }
+  __device__ static void put(uint4& v, int i, float lo, float hi) { reinterpret_cast<uint32_t*>(&v)[i] = pack_bf16x2(lo, hi); }
+  // running maximum of pairs; a NaN is passed over here and met again in the sum
+  using Max = __nv_bfloat162;
+  __device__ static Max max_init() { return __float2bfloat162_rn(-INFINITY); }
+  __device__ static void max_add(Max& m, const uint4& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __hmax2(m, reinterpret_cast<const __nv_bfloat162*>(&v)[i]);
+  }
+  __device__ static float max_get(Max m) { return fmaxf(__low2float(m), __high2float(m)); }
 };
 template <>
 struct LogitTraits<__half> {
@@ -54,24 +63,18 @@ struct LogitTraits<__half> {
   static constexpr uint32_t NEG_INF = 0xfc00fc00u;
   __device__ static float load(const __half* p) { return __half2float(*p); }
   __device__ static __half round(float v) { return __float2half_rn(v); }
-  __device__ static void unpack(const uint4& v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-      f[2 * e] = t.x;
-      f[2 * e + 1] = t.y;
-    }
+  __device__ static uint64_t pair(const uint4& v, int i) {
+    const float2 f = __half22float2(reinterpret_cast<const __half2*>(&v)[i]);
+    return f32x2(f.x, f.y);
   }
-  __device__ static uint4 pack(const float (&o)[8]) {
-    uint32_t w[4];
+  __device__ static void put(uint4& v, int i, float lo, float hi) { reinterpret_cast<__half2*>(&v)[i] = __floats2half2_rn(lo, hi); }
+  using Max = __half2;
+  __device__ static Max max_init() { return __float2half2_rn(-INFINITY); }
+  __device__ static void max_add(Max& m, const uint4& v) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __half2 h = __floats2half2_rn(o[2 * e], o[2 * e + 1]);
-      w[e] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) m = __hmax2(m, reinterpret_cast<const __half2*>(&v)[i]);
   }
+  __device__ static float max_get(Max m) { return fmaxf(__low2float(m), __high2float(m)); }
 };
 template <>
 struct LogitTraits<float> {
@@ -79,15 +82,19 @@ struct LogitTraits<float> {
   static constexpr uint32_t NEG_INF = 0xff800000u;
   __device__ static float load(const float* p) { return *p; }
   __device__ static float round(float v) { return v; }
-  __device__ static void unpack(const uint4& v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
+  __device__ static uint64_t pair(const uint4& v, int i) {
+    return i == 0 ? f32x2(__uint_as_float(v.x), __uint_as_float(v.y)) : f32x2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  __device__ static uint4 pack(const float (&o)[4]) {
-    return make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3]));
+  __device__ static void put(uint4& v, int i, float lo, float hi) {
+    reinterpret_cast<uint32_t*>(&v)[2 * i] = __float_as_uint(lo);
+    reinterpret_cast<uint32_t*>(&v)[2 * i + 1] = __float_as_uint(hi);
   }
+  using Max = float;
+  __device__ static Max max_init() { return -INFINITY; }
+  __device__ static void max_add(Max& m, const uint4& v) {
+    m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))));
+  }
+  __device__ static float max_get(Max m) { return m; }
 };
 
 enum : int { DT_BF16 = 0, DT_FP16 = 1, DT_FP32 = 2 };
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(POLICY_THREADS) flce_policy_rows_kernel(const 
   for (int i = blockIdx.x * POLICY_THREADS + threadIdx.x; i < a.N; i += gridDim.x * POLICY_THREADS) {
     float rows = 0.f, kl = 0.f, weight = 0.f;
     if (a.y[i] != a.ignore_index) {
-      const PolicyRow p = policy_row(a.pol, i, -static_cast<double>(a.row_loss[i]));
+      const PolicyRow p = policy_row(a.pol, policy_load(a.pol, i), -static_cast<double>(a.row_loss[i]));
       const double s = a.reduction == RED_MEAN ? inv_n
                        : a.reduction == RED_NONE && a.row_scale ? static_cast<double>(a.row_scale[i]) : 1.0;
       rows = static_cast<float>(p.loss);
@@ -234,8 +241,10 @@ __global__ void __launch_bounds__(POLICY_THREADS) flce_policy_rows_kernel(const 
 enum : int {
   LOSS_POLICY = 0,    // clipped policy loss
   LOSS_DISTILL = 1,   // distillation, one softmax (ce == 0 or T == 1)
-  LOSS_DISTILL2 = 2   // distillation at T != 1 mixed with hard labels: a second softmax at T = 1
+  LOSS_DISTILL2 = 2,  // distillation at T != 1 mixed with hard labels: a second softmax at T = 1
+  LOSS_POLICY_ENT = 3 // clipped policy loss with an entropy term in its gradient
 };
+__host__ __device__ constexpr bool is_policy(int loss) { return loss == LOSS_POLICY || loss == LOSS_POLICY_ENT; }
 
 struct LogitArgs {
   const void* z;          // [N][V], row stride ld elements
@@ -277,14 +286,14 @@ template <int LOSS>
 __device__ __forceinline__ void stat_add(RowStat& s, float z, float zs) {
   if (z > s.m) {  // move to the new maximum
     const float d = (s.m - z) * zs, f = ex2_approx(d);
-    if constexpr (LOSS == LOSS_POLICY) s.t = f * (s.t + s.l * fmaxf(d, NEG_BIG));
+    if constexpr (is_policy(LOSS)) s.t = f * (s.t + s.l * fmaxf(d, NEG_BIG));
     if constexpr (LOSS == LOSS_DISTILL2) s.t *= ex2_approx((s.m - z) * LOG2E);
     s.l *= f;
     s.m = z;
   }
   const float d = (z - s.m) * zs, e = ex2_approx(d);
   s.l += e;
-  if constexpr (LOSS == LOSS_POLICY) s.t += e * fmaxf(d, NEG_BIG);
+  if constexpr (is_policy(LOSS)) s.t += e * fmaxf(d, NEG_BIG);
   if constexpr (LOSS == LOSS_DISTILL2) s.t += ex2_approx((z - s.m) * LOG2E);
 }
 
@@ -293,7 +302,7 @@ __device__ __forceinline__ void stat_merge(RowStat& s, const RowStat& o, float z
   const float m = fmaxf(s.m, o.m);
   const float d1 = (s.m - m) * zs, d2 = (o.m - m) * zs;
   const float f1 = ex2_approx(d1), f2 = ex2_approx(d2);
-  if constexpr (LOSS == LOSS_POLICY)
+  if constexpr (is_policy(LOSS))
     s.t = f1 * (s.t + s.l * fmaxf(d1, NEG_BIG)) + f2 * (o.t + o.l * fmaxf(d2, NEG_BIG));
   if constexpr (LOSS == LOSS_DISTILL2)
     s.t = s.t * ex2_approx((s.m - m) * LOG2E) + o.t * ex2_approx((o.m - m) * LOG2E);
@@ -328,7 +337,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
   constexpr int EPC = L::EPC;
   constexpr int WARPS = THREADS / 32;
   extern __shared__ __align__(16) uint8_t dyn[];
-  const int K1 = LOSS == LOSS_POLICY ? 1 : a.K + 1;
+  const int K1 = is_policy(LOSS) ? 1 : a.K + 1;
   int* s_id = reinterpret_cast<int*>(dyn);           // sparse entries' vocabulary ids (-1: none)
   float* s_u = reinterpret_cast<float*>(s_id + K1);  // teacher logits
   float* s_c = s_u + K1;                             // coefficient subtracted at the entry
@@ -359,12 +368,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
     // the gradient row shares the logits' alignment, or its elements are stored one by one
     const bool vec_out = g && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
     const int edge_col = rank == 0 && tid < edges ? (tid < head ? tid : a.V - edges + tid) : -1;
-    auto put = [&](int c, const float (&o)[EPC]) {
+    auto put = [&](int c, const uint4& o) {
       if (vec_out) {
-        st_l2hint_v4(reinterpret_cast<uint4*>(g + head) + c, L::pack(o), once);
+        st_l2hint_v4(reinterpret_cast<uint4*>(g + head) + c, o, once);
       } else {
 #pragma unroll
-        for (int e = 0; e < EPC; ++e) g[head + c * EPC + e] = L::round(o[e]);
+        for (int e = 0; e < EPC; ++e) g[head + c * EPC + e] = reinterpret_cast<const T*>(&o)[e];
       }
     };
 
@@ -374,15 +383,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
       if (rank == 0 && tid == 0) {
         if (y != a.ignore_index) raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
         a.row_acc[row] = 0.0;
-        if constexpr (LOSS == LOSS_POLICY) {
+        if constexpr (is_policy(LOSS)) {
           a.out_logp[row] = a.out_entropy[row] = a.out_kl[row] = 0.f;
         } else if (a.out_rows) {
           a.out_rows[row] = 0.f;
         }
       }
       if (g) {
-        const float zero[EPC] = {};
-        for (int c = c0 + tid; c < c1; c += THREADS) put(c, zero);
+        for (int c = c0 + tid; c < c1; c += THREADS) put(c, make_uint4(0u, 0u, 0u, 0u));
         if (edge_col >= 0) g[edge_col] = L::round(0.f);
       }
       continue;
@@ -397,6 +405,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
                       : make_uint4(L::NEG_INF, L::NEG_INF, L::NEG_INF, L::NEG_INF);
     }
     const float edge = edge_col >= 0 ? L::load(z + edge_col) : -INFINITY;
+    PolicyIn pin{};
+    if (is_policy(LOSS) && tid == 0) pin = policy_load(a.pol, row);
     // the sparse entries: the teacher's, then the target
     for (int k = tid; k < K1; k += THREADS) {
       int id = y;
@@ -418,35 +428,55 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
     // ---- statistics
     RowStat st{-FLT_MAX, 0.f, 0.f};
     for (int c = c0 + NCH * THREADS + tid; c < c1; c += THREADS) {  // beyond the registers
-      float f[EPC];
-      L::unpack(ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + c, l2_evict_normal()), f);
+      const uint4 v = ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + c, l2_evict_normal());
 #pragma unroll
-      for (int e = 0; e < EPC; ++e) stat_add<LOSS>(st, f[e], a.zs);
+      for (int i = 0; i < EPC / 2; ++i) {
+        float lo, hi;
+        f32x2_split(L::pair(v, i), lo, hi);
+        stat_add<LOSS>(st, lo, a.zs);
+        stat_add<LOSS>(st, hi, a.zs);
+      }
     }
-    RowStat w{fmaxf(st.m, edge), 0.f, 0.f};
+    typename L::Max vmax = L::max_init();
 #pragma unroll
-    for (int u = 0; u < NCH; ++u) {
-      float f[EPC];
-      L::unpack(raw[u], f);
-#pragma unroll
-      for (int e = 0; e < EPC; ++e) w.m = fmaxf(w.m, f[e]);
-    }
+    for (int u = 0; u < NCH; ++u) L::max_add(vmax, raw[u]);
+    RowStat w{fmaxf(fmaxf(st.m, edge), L::max_get(vmax)), 0.f, 0.f};
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) w.m = fmaxf(w.m, __shfl_xor_sync(0xffffffffu, w.m, o));
-    auto fold = [&](float x) {
-      const float d = (x - w.m) * a.zs, e = ex2_approx(d);
-      w.l += e;
-      if constexpr (LOSS == LOSS_POLICY) w.t = fmaf(e, fmaxf(d, NEG_BIG), w.t);
-      if constexpr (LOSS == LOSS_DISTILL2) w.t += ex2_approx((x - w.m) * LOG2E);
-    };
+    const uint64_t zs2 = f32x2(a.zs, a.zs), one2 = f32x2(LOG2E, LOG2E);
+    {
+      const uint64_t neg_m2 = f32x2(-w.m, -w.m);
+      uint64_t l2 = 0ull, t2 = 0ull;  // two partial sums each
+      auto fold = [&](uint64_t x) {
+        const uint64_t d0 = add2(x, neg_m2);
+        uint64_t d = mul2(d0, zs2);
+        float lo, hi;
+        f32x2_split(d, lo, hi);
+        if constexpr (is_policy(LOSS)) {  // finite, so that a probability of 0 adds 0 to the entropy
+          lo = max_nan(lo, NEG_BIG);
+          hi = max_nan(hi, NEG_BIG);
+          d = f32x2(lo, hi);
+        }
+        const uint64_t e = f32x2(ex2_approx(lo), ex2_approx(hi));
+        l2 = add2(l2, e);
+        if constexpr (is_policy(LOSS)) t2 = fma2(e, d, t2);
+        if constexpr (LOSS == LOSS_DISTILL2) {
+          f32x2_split(mul2(d0, one2), lo, hi);
+          t2 = add2(t2, f32x2(ex2_approx(lo), ex2_approx(hi)));
+        }
+      };
 #pragma unroll
-    for (int u = 0; u < NCH; ++u) {
-      float f[EPC];
-      L::unpack(raw[u], f);
+      for (int u = 0; u < NCH; ++u) {
 #pragma unroll
-      for (int e = 0; e < EPC; ++e) fold(f[e]);
+        for (int i = 0; i < EPC / 2; ++i) fold(L::pair(raw[u], i));
+      }
+      fold(f32x2(edge, -INFINITY));
+      float lo, hi;
+      f32x2_split(l2, lo, hi);
+      w.l = lo + hi;
+      f32x2_split(t2, lo, hi);
+      w.t = lo + hi;
     }
-    fold(edge);
     if (c1 - c0 > NCH * THREADS) stat_merge<LOSS>(w, st, a.zs);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -489,11 +519,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
       const double s = a.reduction == RED_MEAN ? inv_n
                        : a.reduction == RED_NONE && a.row_scale ? static_cast<double>(a.row_scale[row]) : 1.0;
       double total = 0.0;
-      if constexpr (LOSS == LOSS_POLICY) {
+      if constexpr (is_policy(LOSS)) {
         if (lane == 0) {
           const double lp = (static_cast<double>(s_z[0]) - m) * a.inv_T - lnL;
           const double H = lnL - static_cast<double>(w.t) / static_cast<double>(w.l) * LN2;
-          const PolicyRow p = policy_row(a.pol, row, lp);
+          const PolicyRow p = policy_row(a.pol, pin, lp);
           total = p.loss;
           double a0 = -p.dlogp, a1 = 0.0;
           if (a.ent_coef != 0.0) {
@@ -553,32 +583,54 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
 
     // ---- the gradient
     if (g) {
+      // Unpack the chunks anew here: values kept unpacked since the sums would
+      // take twice the registers, and spill.
+#pragma unroll
+      for (int u = 0; u < NCH; ++u)
+        asm volatile("" : "+r"(raw[u].x), "+r"(raw[u].y), "+r"(raw[u].z), "+r"(raw[u].w));
       const RowCoef c = coef;
       const float m = w.m;
+      const uint64_t neg_m2 = f32x2(-m, -m), a2 = f32x2(c.a, c.a), b2 = f32x2(c.b, c.b);
+      auto dense2 = [&](uint64_t x) {
+        const uint64_t d0 = add2(x, neg_m2);
+        uint64_t d = mul2(d0, zs2);
+        float lo, hi;
+        f32x2_split(d, lo, hi);
+        if constexpr (LOSS == LOSS_POLICY_ENT) {
+          lo = max_nan(lo, NEG_BIG);
+          hi = max_nan(hi, NEG_BIG);
+          d = f32x2(lo, hi);
+        }
+        const uint64_t e = f32x2(ex2_approx(lo), ex2_approx(hi));
+        if constexpr (LOSS == LOSS_POLICY_ENT) return mul2(e, fma2(b2, d, a2));
+        if constexpr (LOSS == LOSS_DISTILL2) {
+          f32x2_split(mul2(d0, one2), lo, hi);
+          return fma2(f32x2(ex2_approx(lo), ex2_approx(hi)), b2, mul2(e, a2));
+        }
+        return mul2(e, a2);
+      };
       auto dense = [&](float x) {
-        const float d = (x - m) * a.zs, e = ex2_approx(d);
-        if constexpr (LOSS == LOSS_POLICY) return e * fmaf(c.b, fmaxf(d, NEG_BIG), c.a);
-        if constexpr (LOSS == LOSS_DISTILL2) return fmaf(e, c.a, ex2_approx((x - m) * LOG2E) * c.b);
-        return e * c.a;
+        float lo, hi;
+        f32x2_split(dense2(f32x2(x, x)), lo, hi);
+        return lo;
+      };
+      auto grad_chunk = [&](int ch, const uint4& v) {
+        uint4 o;
+#pragma unroll
+        for (int i = 0; i < EPC / 2; ++i) {
+          float lo, hi;
+          f32x2_split(dense2(L::pair(v, i)), lo, hi);
+          L::put(o, i, lo, hi);
+        }
+        put(ch, o);
       };
 #pragma unroll
       for (int u = 0; u < NCH; ++u) {
         const int ch = c0 + u * THREADS + tid;
-        if (ch < c1) {
-          float f[EPC];
-          L::unpack(raw[u], f);
-#pragma unroll
-          for (int e = 0; e < EPC; ++e) f[e] = dense(f[e]);
-          put(ch, f);
-        }
+        if (ch < c1) grad_chunk(ch, raw[u]);
       }
-      for (int ch = c0 + NCH * THREADS + tid; ch < c1; ch += THREADS) {
-        float f[EPC];
-        L::unpack(ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + ch, once), f);
-#pragma unroll
-        for (int e = 0; e < EPC; ++e) f[e] = dense(f[e]);
-        put(ch, f);
-      }
+      for (int ch = c0 + NCH * THREADS + tid; ch < c1; ch += THREADS)
+        grad_chunk(ch, ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + ch, once));
       if (edge_col >= 0) g[edge_col] = L::round(dense(edge));
       __syncthreads();
       // The sparse entries of this CTA's part; equal ids add up, and each of
