@@ -353,7 +353,8 @@ flce_status_t flce_clipped_policy(const float* d_row_loss, const int32_t* y, int
  *   L_i as above - entropy_coef H_i;
  * dlogits = d loss / d z (temperature's 1/T included).  d_logp, d_entropy and
  * d_kl (DEVICE fp32 [N]) receive lp, H and kl, 0 on ignored rows.  A logit of
- * -infinity is a vocabulary entry of probability 0.  Targets outside [0, V) set
+ * -infinity is a vocabulary entry of probability 0; lower finite logits than
+ * -2^100 count as -2^100.  Targets outside [0, V) set
  * FLCE_ERR_TARGET_OUT_OF_RANGE in d_status and count as ignored in the sums.
  * workspace: flce_ce_workspace_size(N, V) bytes.  Asynchronous; may be
  * captured in a CUDA graph. */

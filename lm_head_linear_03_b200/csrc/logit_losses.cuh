@@ -31,6 +31,11 @@
 namespace flce {
 
 constexpr int DISTILL_MAX_K = 1024;
+// Lower logits count as LOGIT_LOWEST in the policy loss, whose sums hold e (z - m):
+// the difference stays finite, so that a probability of 0 adds 0.  Registers
+// without a logit hold LOGIT_NONE, which has probability 0 beside any logit.
+// Powers of two: the same value in bf16.
+constexpr float LOGIT_LOWEST = -0x1p100f, LOGIT_NONE = -0x1p102f;
 constexpr float NEG_BIG = -1e4f;  // exponents below this are 0 in every format; finite, so that 0 * it is 0
 
 // ------------------------------------------------------- logits by type --
@@ -48,6 +53,21 @@ struct LogitTraits<__nv_bfloat16> {
     return f32x2(bf16lo_to_f32(w), bf16hi_to_f32(w));
   }
   __device__ static void put(uint4& v, int i, float lo, float hi) { reinterpret_cast<uint32_t*>(&v)[i] = pack_bf16x2(lo, hi); }
+  // CLAMPS: the type can hold LOGIT_LOWEST.  clamp raises a chunk to it (a NaN
+  // stays), none() is a chunk without logits.
+  static constexpr bool CLAMPS = true;
+  __device__ static void clamp(uint4& v) {
+    const __nv_bfloat162 lowest = __float2bfloat162_rn(LOGIT_LOWEST);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162& h = reinterpret_cast<__nv_bfloat162*>(&v)[i];
+      h = __hmax2_nan(h, lowest);
+    }
+  }
+  __device__ static uint4 none() {
+    const uint32_t w = pack_bf16x2(LOGIT_NONE, LOGIT_NONE);
+    return make_uint4(w, w, w, w);
+  }
   // running maximum of pairs; a NaN is passed over here and met again in the sum
   using Max = __nv_bfloat162;
   __device__ static Max max_init() { return __float2bfloat162_rn(-INFINITY); }
@@ -67,6 +87,9 @@ struct LogitTraits<__half> {
     const float2 f = __half22float2(reinterpret_cast<const __half2*>(&v)[i]);
     return f32x2(f.x, f.y);
   }
+  static constexpr bool CLAMPS = false;  // 65504 is too near for that at a high temperature
+  __device__ static void clamp(uint4&) {}
+  __device__ static uint4 none() { return make_uint4(NEG_INF, NEG_INF, NEG_INF, NEG_INF); }
   __device__ static void put(uint4& v, int i, float lo, float hi) { reinterpret_cast<__half2*>(&v)[i] = __floats2half2_rn(lo, hi); }
   using Max = __half2;
   __device__ static Max max_init() { return __float2half2_rn(-INFINITY); }
@@ -84,6 +107,18 @@ struct LogitTraits<float> {
   __device__ static float round(float v) { return v; }
   __device__ static uint64_t pair(const uint4& v, int i) {
     return i == 0 ? f32x2(__uint_as_float(v.x), __uint_as_float(v.y)) : f32x2(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  static constexpr bool CLAMPS = true;
+  __device__ static void clamp(uint4& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t& w = reinterpret_cast<uint32_t*>(&v)[i];
+      w = __float_as_uint(max_nan(__uint_as_float(w), LOGIT_LOWEST));
+    }
+  }
+  __device__ static uint4 none() {
+    const uint32_t w = __float_as_uint(LOGIT_NONE);
+    return make_uint4(w, w, w, w);
   }
   __device__ static void put(uint4& v, int i, float lo, float hi) {
     reinterpret_cast<uint32_t*>(&v)[2 * i] = __float_as_uint(lo);
@@ -397,14 +432,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
     }
 
     // ---- the row's part of this CTA
+    const uint4* zt = reinterpret_cast<const uint4*>(zc) + (c0 + tid);
+    const int mine = c1 - c0 - tid;  // chunks from this thread's first on: u * THREADS < mine
     uint4 raw[NCH];
 #pragma unroll
-    for (int u = 0; u < NCH; ++u) {
-      const int c = c0 + u * THREADS + tid;
-      raw[u] = c < c1 ? ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + c, once)
-                      : make_uint4(L::NEG_INF, L::NEG_INF, L::NEG_INF, L::NEG_INF);
-    }
-    const float edge = edge_col >= 0 ? L::load(z + edge_col) : -INFINITY;
+    for (int u = 0; u < NCH; ++u)
+      raw[u] = u * THREADS < mine ? ld_l2hint_v4(zt + u * THREADS, once)
+                                  : make_uint4(L::NEG_INF, L::NEG_INF, L::NEG_INF, L::NEG_INF);
+    auto lifted = [&](float x) { return is_policy(LOSS) ? max_nan(x, LOGIT_LOWEST) : x; };
+    const float none = is_policy(LOSS) ? LOGIT_NONE : -INFINITY;
+    float edge = edge_col >= 0 ? L::load(z + edge_col) : -INFINITY;
     PolicyIn pin{};
     if (is_policy(LOSS) && tid == 0) pin = policy_load(a.pol, row);
     // the sparse entries: the teacher's, then the target
@@ -426,6 +463,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
     }
 
     // ---- statistics
+    float top = edge;  // this thread's largest logit as it stands
     RowStat st{-FLT_MAX, 0.f, 0.f};
     for (int c = c0 + NCH * THREADS + tid; c < c1; c += THREADS) {  // beyond the registers
       const uint4 v = ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + c, l2_evict_normal());
@@ -433,16 +471,29 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
       for (int i = 0; i < EPC / 2; ++i) {
         float lo, hi;
         f32x2_split(L::pair(v, i), lo, hi);
-        stat_add<LOSS>(st, lo, a.zs);
-        stat_add<LOSS>(st, hi, a.zs);
+        top = fmaxf(top, fmaxf(lo, hi));
+        stat_add<LOSS>(st, lifted(lo), a.zs);
+        stat_add<LOSS>(st, lifted(hi), a.zs);
       }
     }
     typename L::Max vmax = L::max_init();
 #pragma unroll
     for (int u = 0; u < NCH; ++u) L::max_add(vmax, raw[u]);
-    RowStat w{fmaxf(fmaxf(st.m, edge), L::max_get(vmax)), 0.f, 0.f};
+    top = fmaxf(top, L::max_get(vmax));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) w.m = fmaxf(w.m, __shfl_xor_sync(0xffffffffu, w.m, o));
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // -FLT_MAX, not -infinity, so that the differences below are never NaN for it
+    RowStat w{fmaxf(top, is_policy(LOSS) ? LOGIT_LOWEST : -FLT_MAX), 0.f, 0.f};
+    if constexpr (is_policy(LOSS)) {
+#pragma unroll
+      for (int u = 0; u < NCH; ++u) {
+        if (u * THREADS < mine)
+          L::clamp(raw[u]);
+        else
+          raw[u] = L::none();
+      }
+      edge = edge_col >= 0 ? lifted(edge) : none;
+    }
     const uint64_t zs2 = f32x2(a.zs, a.zs), one2 = f32x2(LOG2E, LOG2E);
     {
       const uint64_t neg_m2 = f32x2(-w.m, -w.m);
@@ -452,7 +503,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
         uint64_t d = mul2(d0, zs2);
         float lo, hi;
         f32x2_split(d, lo, hi);
-        if constexpr (is_policy(LOSS)) {  // finite, so that a probability of 0 adds 0 to the entropy
+        if constexpr (is_policy(LOSS) && !L::CLAMPS) {  // finite, so that a probability of 0 adds 0 to the entropy
           lo = max_nan(lo, NEG_BIG);
           hi = max_nan(hi, NEG_BIG);
           d = f32x2(lo, hi);
@@ -470,7 +521,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
 #pragma unroll
         for (int i = 0; i < EPC / 2; ++i) fold(L::pair(raw[u], i));
       }
-      fold(f32x2(edge, -INFINITY));
+      fold(f32x2(edge, none));
       float lo, hi;
       f32x2_split(l2, lo, hi);
       w.l = lo + hi;
@@ -484,11 +535,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
       w.t += __shfl_xor_sync(0xffffffffu, w.t, o);
     }
     if (cs == 1) {
-      if (lane == 0) rec[parity][warp] = make_float4(w.m, w.l, w.t, 0.f);
+      if (lane == 0) rec[parity][warp] = make_float4(w.m, w.l, w.t, top);
       __syncthreads();
     } else {
       if (lane < cs)
-        st_cluster_f4(mapa_shared(smem_u32(&rec[parity][rank * WARPS + warp]), lane), make_float4(w.m, w.l, w.t, 0.f));
+        st_cluster_f4(mapa_shared(smem_u32(&rec[parity][rank * WARPS + warp]), lane), make_float4(w.m, w.l, w.t, top));
       cluster_sync_all();
     }
 
@@ -500,8 +551,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
     for (int o = 16; o > 0; o >>= 1) w.m = fmaxf(w.m, __shfl_xor_sync(0xffffffffu, w.m, o));
     if (warp == 0) {
       w.l = w.t = 0.f;
+      top = -INFINITY;
       for (int r = lane; r < records; r += 32) {
         const float4 v = rec[parity][r];
+        top = fmaxf(top, v.w);
         RowStat o{w.m, 0.f, 0.f};
         stat_merge<LOSS>(o, RowStat{v.x, v.y, v.z}, a.zs);
         w.l += o.l;
@@ -512,6 +565,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
         w.l += __shfl_xor_sync(0xffffffffu, w.l, o);
         w.t += __shfl_xor_sync(0xffffffffu, w.t, o);
       }
+      if (is_policy(LOSS) && !__any_sync(0xffffffffu, top > -INFINITY)) w.l = 0.f;  // every logit is -infinity: NaN
       // Log-probabilities as (z - m)/T - ln L: the difference first, so that a
       // row whose every logit is the type's lowest value still has one.
       const double m = static_cast<double>(w.m);
@@ -521,8 +575,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
       double total = 0.0;
       if constexpr (is_policy(LOSS)) {
         if (lane == 0) {
-          const double lp = (static_cast<double>(s_z[0]) - m) * a.inv_T - lnL;
-          const double H = lnL - static_cast<double>(w.t) / static_cast<double>(w.l) * LN2;
+          const float zy = s_z[0] == -INFINITY ? s_z[0] : lifted(s_z[0]);
+          const double lp = (static_cast<double>(zy) - m) * a.inv_T - lnL;
+          const double inv_l = 1.0 / static_cast<double>(w.l);
+          const double H = lnL - static_cast<double>(w.t) * inv_l * LN2;
           const PolicyRow p = policy_row(a.pol, pin, lp);
           total = p.loss;
           double a0 = -p.dlogp, a1 = 0.0;
@@ -533,8 +589,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
           }
           const double f = s * a.inv_T;
           s_c[0] = static_cast<float>(-p.dlogp * f);
-          coef.a = static_cast<float>(a0 * f / static_cast<double>(w.l));
-          coef.b = static_cast<float>(a1 * f / static_cast<double>(w.l));
+          coef.a = static_cast<float>(a0 * f * inv_l);
+          coef.b = static_cast<float>(a1 * f * inv_l);
           if (rank == 0) {
             a.out_logp[row] = static_cast<float>(lp);
             a.out_entropy[row] = static_cast<float>(H);
@@ -596,7 +652,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
         uint64_t d = mul2(d0, zs2);
         float lo, hi;
         f32x2_split(d, lo, hi);
-        if constexpr (LOSS == LOSS_POLICY_ENT) {
+        if constexpr (LOSS == LOSS_POLICY_ENT && !L::CLAMPS) {
           lo = max_nan(lo, NEG_BIG);
           hi = max_nan(hi, NEG_BIG);
           d = f32x2(lo, hi);
@@ -614,7 +670,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
         f32x2_split(dense2(f32x2(x, x)), lo, hi);
         return lo;
       };
-      auto grad_chunk = [&](int ch, const uint4& v) {
+      auto grad_chunk = [&](const uint4& v) {
         uint4 o;
 #pragma unroll
         for (int i = 0; i < EPC / 2; ++i) {
@@ -622,15 +678,23 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
           f32x2_split(dense2(L::pair(v, i)), lo, hi);
           L::put(o, i, lo, hi);
         }
-        put(ch, o);
+        return o;
       };
+      if (vec_out) {
+        uint4* gt = reinterpret_cast<uint4*>(g + head) + (c0 + tid);
 #pragma unroll
-      for (int u = 0; u < NCH; ++u) {
-        const int ch = c0 + u * THREADS + tid;
-        if (ch < c1) grad_chunk(ch, raw[u]);
+        for (int u = 0; u < NCH; ++u)
+          if (u * THREADS < mine) st_l2hint_v4(gt + u * THREADS, grad_chunk(raw[u]), once);
+      } else {
+#pragma unroll
+        for (int u = 0; u < NCH; ++u)
+          if (u * THREADS < mine) put(c0 + u * THREADS + tid, grad_chunk(raw[u]));
       }
-      for (int ch = c0 + NCH * THREADS + tid; ch < c1; ch += THREADS)
-        grad_chunk(ch, ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + ch, once));
+      for (int ch = c0 + NCH * THREADS + tid; ch < c1; ch += THREADS) {
+        uint4 v = ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + ch, once);
+        if constexpr (is_policy(LOSS)) L::clamp(v);
+        put(ch, grad_chunk(v));
+      }
       if (edge_col >= 0) g[edge_col] = L::round(dense(edge));
       __syncthreads();
       // The sparse entries of this CTA's part; equal ids add up, and each of
@@ -643,7 +707,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
         float c_sum = 0.f;
         for (int i = 0; i < K1; ++i)
           if (s_id[i] == id) c_sum += s_c[i];
-        g[id] = L::round(dense(s_z[k]) - c_sum);
+        g[id] = L::round(dense(lifted(s_z[k])) - c_sum);
       }
     }
     __syncthreads();  // the shared row data is reused
