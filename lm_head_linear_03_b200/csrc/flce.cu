@@ -876,23 +876,35 @@ flce_status_t begin_rows(const int32_t* y, int64_t N, int32_t ignore_index, uint
   return cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
 }
 
-// How a row of `V` elements is laid over a cluster (see the kernel).
-struct LogitShape {
-  int cluster, threads, nch;
-};
-LogitShape logit_shape(int64_t N, int64_t V, int es, int num_sms) {
-  const int64_t chunks = V * es / 16 + 1;
+// CTAs per row (see the kernel): one, unless there are too few rows for the SMs,
+// or rows so long that those under way would not fit in L2 together.
+constexpr int64_t LOGIT_PART_BYTES = 256 * 1024;  // of a row, per CTA
+int logit_cluster(int64_t N, int64_t V, int es, int num_sms) {
   int cs = 1;
-  while (cs < LOGIT_MAX_CLUSTER && (chunks > cs * 2048 || (N * cs * 2 <= num_sms && chunks > cs * 512))) cs *= 2;
-  const int64_t per = (chunks + cs - 1) / cs;
-  return {cs, per > 2048 ? 512 : 256, per > 512 ? 8 : 2};
+  while (cs < LOGIT_MAX_CLUSTER && (V * es > cs * LOGIT_PART_BYTES || (N * cs < num_sms && V * es > cs * 8192))) cs *= 2;
+  return cs;
 }
 
-template <typename T, int LOSS, int THREADS, int NCH>
-cudaError_t launch_logit_shape(const LogitArgs& a, int cs, size_t smem, cudaStream_t stream) {
+// Clusters of a kernel that run at the same time: the persistent grid.  Asked of
+// the runtime once per device, kernel, cluster size and shared memory.
+std::mutex g_fit_mu;
+struct LogitFit {
+  const void* kernel;
+  size_t smem;
+  int dev, cs, clusters;
+};
+constexpr int MAX_FITS = 256;
+LogitFit g_fit[MAX_FITS];
+int g_fits = 0;
+
+template <typename T, int LOSS>
+cudaError_t launch_logit_type(const LogitArgs& a, int num_sms, int dev, size_t smem, cudaStream_t stream) {
+  const auto kernel = flce_logit_loss_kernel<T, LOSS>;
+  const int cs = logit_cluster(a.N, a.V, sizeof(T), num_sms);
+  smem += LOGIT_RING_BYTES;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(a.N, 1 << 20) * cs), 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(cs), 1, 1);
+  cfg.blockDim = dim3(LOGIT_THREADS, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -902,22 +914,32 @@ cudaError_t launch_logit_shape(const LogitArgs& a, int cs, size_t smem, cudaStre
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, flce_logit_loss_kernel<T, LOSS, THREADS, NCH>, a);
-}
-
-template <typename T, int LOSS>
-cudaError_t launch_logit_type(const LogitArgs& a, int num_sms, size_t smem, cudaStream_t stream) {
-  const LogitShape h = logit_shape(a.N, a.V, sizeof(T), num_sms);
-  if (h.threads == 512) return launch_logit_shape<T, LOSS, 512, 8>(a, h.cluster, smem, stream);
-  if (h.nch == 8) return launch_logit_shape<T, LOSS, 256, 8>(a, h.cluster, smem, stream);
-  return launch_logit_shape<T, LOSS, 256, 2>(a, h.cluster, smem, stream);
+  int fit = 0;
+  {
+    const void* id = reinterpret_cast<const void*>(kernel);
+    std::lock_guard<std::mutex> lk(g_fit_mu);
+    for (int k = 0; k < g_fits && !fit; ++k)
+      if (g_fit[k].kernel == id && g_fit[k].smem == smem && g_fit[k].dev == dev && g_fit[k].cs == cs)
+        fit = g_fit[k].clusters;
+    if (!fit) {
+      cudaError_t e;
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LOGIT_RING_BYTES + 32 * (DISTILL_MAX_K + 1))) !=
+              cudaSuccess ||
+          (e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg)) != cudaSuccess)
+        return e;
+      if (fit <= 0) return cudaErrorInvalidConfiguration;
+      if (g_fits < MAX_FITS) g_fit[g_fits++] = {id, smem, dev, cs, fit};
+    }
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(a.N, fit) * cs), 1, 1);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <int LOSS>
-cudaError_t launch_logit_loss(const LogitArgs& a, int dtype, int num_sms, size_t smem, cudaStream_t stream) {
-  if (dtype == FLCE_DTYPE_BF16) return launch_logit_type<__nv_bfloat16, LOSS>(a, num_sms, smem, stream);
-  if (dtype == FLCE_DTYPE_FP16) return launch_logit_type<__half, LOSS>(a, num_sms, smem, stream);
-  return launch_logit_type<float, LOSS>(a, num_sms, smem, stream);
+cudaError_t launch_logit_loss(const LogitArgs& a, int dtype, int num_sms, int dev, size_t smem, cudaStream_t stream) {
+  if (dtype == FLCE_DTYPE_BF16) return launch_logit_type<__nv_bfloat16, LOSS>(a, num_sms, dev, smem, stream);
+  if (dtype == FLCE_DTYPE_FP16) return launch_logit_type<__half, LOSS>(a, num_sms, dev, smem, stream);
+  return launch_logit_type<float, LOSS>(a, num_sms, dev, smem, stream);
 }
 
 // What the two losses on logits share: device check, counters, launch.
@@ -932,15 +954,16 @@ flce_status_t enqueue_logit_loss(LogitArgs& a, int loss, int32_t dtype, uint8_t*
   a.ticket = reinterpret_cast<unsigned int*>(ws + L.ctrl + 4);
   a.n_valid = reinterpret_cast<const int*>(ws + L.ctrl + 8);
   a.row_acc = reinterpret_cast<double*>(ws + L.row_acc);
-  const size_t smem = 16 * (is_policy(loss) ? 1 : static_cast<size_t>(a.K) + 1);
+  a.timeout_ns = DEFAULT_TIMEOUT_NS;
+  const size_t smem = is_policy(loss) ? 0 : 2 * 16 * (static_cast<size_t>(a.K) + 1);
   size_t slot;
   prof_begin(stream, KIND_LOGIT_LOSS, &slot);
   cudaError_t e;
   switch (loss) {
-    case LOSS_POLICY: e = launch_logit_loss<LOSS_POLICY>(a, dtype, di.num_sms, smem, stream); break;
-    case LOSS_POLICY_ENT: e = launch_logit_loss<LOSS_POLICY_ENT>(a, dtype, di.num_sms, smem, stream); break;
-    case LOSS_DISTILL: e = launch_logit_loss<LOSS_DISTILL>(a, dtype, di.num_sms, smem, stream); break;
-    default: e = launch_logit_loss<LOSS_DISTILL2>(a, dtype, di.num_sms, smem, stream); break;
+    case LOSS_POLICY: e = launch_logit_loss<LOSS_POLICY>(a, dtype, di.num_sms, dev, smem, stream); break;
+    case LOSS_POLICY_ENT: e = launch_logit_loss<LOSS_POLICY_ENT>(a, dtype, di.num_sms, dev, smem, stream); break;
+    case LOSS_DISTILL: e = launch_logit_loss<LOSS_DISTILL>(a, dtype, di.num_sms, dev, smem, stream); break;
+    default: e = launch_logit_loss<LOSS_DISTILL2>(a, dtype, di.num_sms, dev, smem, stream); break;
   }
   prof_end(stream, slot);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);

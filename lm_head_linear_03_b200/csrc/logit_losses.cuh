@@ -32,8 +32,8 @@ namespace flce {
 
 constexpr int DISTILL_MAX_K = 1024;
 // Lower logits count as LOGIT_LOWEST in the policy loss, whose sums hold e (z - m):
-// the difference stays finite, so that a probability of 0 adds 0.  Registers
-// without a logit hold LOGIT_NONE, which has probability 0 beside any logit.
+// the difference stays finite, so that a probability of 0 adds 0.  A register
+// without a logit holds LOGIT_NONE, which has probability 0 beside any logit.
 // Powers of two: the same value in bf16.
 constexpr float LOGIT_LOWEST = -0x1p100f, LOGIT_NONE = -0x1p102f;
 constexpr float NEG_BIG = -1e4f;  // exponents below this are 0 in every format; finite, so that 0 * it is 0
@@ -45,7 +45,6 @@ struct LogitTraits;  // a 16-byte chunk of logits: unpacked in pairs, packed, it
 template <>
 struct LogitTraits<__nv_bfloat16> {
   static constexpr int EPC = 8;  // elements of a chunk
-  static constexpr uint32_t NEG_INF = 0xff80ff80u;
   __device__ static float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   __device__ static __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
   __device__ static uint64_t pair(const uint4& v, int i) {
@@ -53,8 +52,7 @@ struct LogitTraits<__nv_bfloat16> {
     return f32x2(bf16lo_to_f32(w), bf16hi_to_f32(w));
   }
   __device__ static void put(uint4& v, int i, float lo, float hi) { reinterpret_cast<uint32_t*>(&v)[i] = pack_bf16x2(lo, hi); }
-  // CLAMPS: the type can hold LOGIT_LOWEST.  clamp raises a chunk to it (a NaN
-  // stays), none() is a chunk without logits.
+  // CLAMPS: the type can hold LOGIT_LOWEST; clamp raises a chunk to it (a NaN stays)
   static constexpr bool CLAMPS = true;
   __device__ static void clamp(uint4& v) {
     const __nv_bfloat162 lowest = __float2bfloat162_rn(LOGIT_LOWEST);
@@ -63,10 +61,6 @@ struct LogitTraits<__nv_bfloat16> {
       __nv_bfloat162& h = reinterpret_cast<__nv_bfloat162*>(&v)[i];
       h = __hmax2_nan(h, lowest);
     }
-  }
-  __device__ static uint4 none() {
-    const uint32_t w = pack_bf16x2(LOGIT_NONE, LOGIT_NONE);
-    return make_uint4(w, w, w, w);
   }
   // running maximum of pairs; a NaN is passed over here and met again in the sum
   using Max = __nv_bfloat162;
@@ -80,7 +74,6 @@ struct LogitTraits<__nv_bfloat16> {
 template <>
 struct LogitTraits<__half> {
   static constexpr int EPC = 8;
-  static constexpr uint32_t NEG_INF = 0xfc00fc00u;
   __device__ static float load(const __half* p) { return __half2float(*p); }
   __device__ static __half round(float v) { return __float2half_rn(v); }
   __device__ static uint64_t pair(const uint4& v, int i) {
@@ -89,7 +82,6 @@ struct LogitTraits<__half> {
   }
   static constexpr bool CLAMPS = false;  // 65504 is too near for that at a high temperature
   __device__ static void clamp(uint4&) {}
-  __device__ static uint4 none() { return make_uint4(NEG_INF, NEG_INF, NEG_INF, NEG_INF); }
   __device__ static void put(uint4& v, int i, float lo, float hi) { reinterpret_cast<__half2*>(&v)[i] = __floats2half2_rn(lo, hi); }
   using Max = __half2;
   __device__ static Max max_init() { return __float2half2_rn(-INFINITY); }
@@ -102,7 +94,6 @@ struct LogitTraits<__half> {
 template <>
 struct LogitTraits<float> {
   static constexpr int EPC = 4;
-  static constexpr uint32_t NEG_INF = 0xff800000u;
   __device__ static float load(const float* p) { return *p; }
   __device__ static float round(float v) { return v; }
   __device__ static uint64_t pair(const uint4& v, int i) {
@@ -115,10 +106,6 @@ struct LogitTraits<float> {
       uint32_t& w = reinterpret_cast<uint32_t*>(&v)[i];
       w = __float_as_uint(max_nan(__uint_as_float(w), LOGIT_LOWEST));
     }
-  }
-  __device__ static uint4 none() {
-    const uint32_t w = __float_as_uint(LOGIT_NONE);
-    return make_uint4(w, w, w, w);
   }
   __device__ static void put(uint4& v, int i, float lo, float hi) {
     reinterpret_cast<uint32_t*>(&v)[2 * i] = __float_as_uint(lo);
@@ -295,6 +282,7 @@ struct LogitArgs {
   int* status;
   double inv_T;
   float zs;               // log2(e) / T
+  unsigned long long timeout_ns;
   // policy
   PolicyArgs pol;
   double ent_coef;
@@ -345,76 +333,173 @@ __device__ __forceinline__ void stat_merge(RowStat& s, const RowStat& o, float z
   s.m = m;
 }
 
-// What the gradient pass needs of a row.
+// What the gradient needs of a row.
 struct RowCoef {
+  float m;       // the row's maximum
   float a, b;    // dense part: e (a + b arg), or a e + b e1 with two softmaxes
+  float c, zy;   // policy: subtracted at the target, and the logit there
 };
 
+constexpr int LOGIT_THREADS = 256;
+constexpr int LOGIT_WARPS = LOGIT_THREADS / 32;
 constexpr int LOGIT_MAX_CLUSTER = 8;
+constexpr int TILE_CHUNKS = 256;  // 16-byte chunks of a warp's tile (4 KB), eight per lane
+constexpr int TILE_STAGES = 3;    // tiles per warp in shared memory
+constexpr int LOGIT_RING_BYTES = LOGIT_WARPS * TILE_STAGES * TILE_CHUNKS * 16;
 
-// A row is split over the CTAs of a cluster, each of which holds its part in
-// registers: 16-byte chunks on 16-byte boundaries, NCH per thread, so the
-// logits are read from memory once and all of a thread's loads are in flight
-// together.  (What lies beyond the registers, in rows longer than
-// cluster * THREADS * NCH chunks, is read a second time for the gradient.)
-// The up to 2 * (EPC - 1) elements in front of the first and behind the last
-// boundary are held one per thread by the cluster's first CTA.
+// Where row `row` lies, and which of it is CTA `rank`'s part.  Bulk copies move
+// 16-byte chunks on 16-byte boundaries: the up to 2 * (EPC - 1) elements in
+// front of the first and behind the last boundary ("edges") are held one per
+// thread by the cluster's first CTA.
+template <typename T>
+struct RowPart {
+  static constexpr int EPC = LogitTraits<T>::EPC;
+  const T* z;
+  T* g;
+  int head, edges;  // elements before the first boundary, elements outside chunks
+  int n;            // this CTA's chunks
+  int col0;         // column of the first one
+  int tiles;        // tiles of the calling warp: those j < ceil(n / TILE_CHUNKS) with j % LOGIT_WARPS == warp
+  bool vec_out;     // the gradient row shares the logits' alignment
+  __device__ RowPart(const LogitArgs& a, int row, int rank, int cs, int warp) {
+    z = static_cast<const T*>(a.z) + static_cast<long long>(row) * a.ld;
+    g = a.g ? static_cast<T*>(a.g) + static_cast<long long>(row) * a.ldg : nullptr;
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
+    head = min(a.V, mis ? EPC - mis : 0);
+    const int chunks = (a.V - head) / EPC;
+    edges = a.V - chunks * EPC;
+    const int per = (chunks + cs - 1) / cs;
+    const int c0 = min(chunks, rank * per);
+    n = min(per, chunks - c0);
+    col0 = head + c0 * EPC;
+    const int all = (n + TILE_CHUNKS - 1) / TILE_CHUNKS;
+    tiles = all > warp ? (all - warp + LOGIT_WARPS - 1) / LOGIT_WARPS : 0;
+    vec_out = g && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
+  }
+  __device__ bool has(int id) const { return id >= col0 && id < col0 + n * EPC; }
+  // first chunk and chunk count of the calling warp's k-th tile
+  __device__ int tile_at(int k, int warp) const { return (k * LOGIT_WARPS + warp) * TILE_CHUNKS; }
+  __device__ int tile_size(int at) const { return min(TILE_CHUNKS, n - at); }
+  __device__ int edge_col(const LogitArgs& a, int rank, int tid) const {
+    return rank == 0 && tid < edges ? (tid < head ? tid : a.V - edges + tid) : -1;
+  }
+};
+
+__device__ __forceinline__ bool row_counts(const LogitArgs& a, int y) {
+  return y != a.ignore_index && y >= 0 && y < a.V;
+}
+
+// Persistent CTAs, each with a row (or, in clusters, its part of a row) at a
+// time.  A row is walked twice: forwards for its maximum and sums, backwards
+// for the gradient.  The second read finds the row in L2, where the first one's
+// policy keeps it: the rows under way on all SMs are some 80 MB at most (the
+// host gives longer rows to clusters).  Memory is thus read and written once,
+// and what a row costs beside its elements (two exchanges, the fp64 of its
+// scalars) is paid once per 100,000 elements or so.
 //
-// Statistics: each warp folds its elements under its own maximum and writes one
-// record into every CTA of the cluster; after one cluster barrier every warp
-// merges all records in a fixed order, so all CTAs know the row's totals
-// without a second exchange.  Warp 0 turns them into the row's outputs (first
-// CTA) and the gradient's coefficients; then each CTA writes its part of the
-// gradient and, behind a CTA barrier, the sparse entries that lie in it.
-template <typename T, int LOSS, int THREADS, int NCH>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kernel(const LogitArgs a) {
+// Every warp moves its own tiles of 4 KB through a ring of its own in shared
+// memory: one lane issues the bulk copies, the next tiles (of the second walk,
+// and of the next row) are under way while this one is worked on, and a tile
+// waits for no other warp.  Gradient tiles are written in place of the logits
+// and leave by bulk copies too.
+//
+// Statistics: lanes fold under maxima of their own, warps write one record each
+// into every CTA of the cluster, and behind one barrier every warp merges the
+// maxima and warp 0 of each CTA the sums, in a fixed order, so all CTAs find the
+// same totals.  Warp 0 turns them into the row's outputs (first CTA) and the
+// gradient's coefficients.
+template <typename T, int LOSS>
+__global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const LogitArgs a) {
   using L = LogitTraits<T>;
   constexpr int EPC = L::EPC;
-  constexpr int WARPS = THREADS / 32;
-  extern __shared__ __align__(16) uint8_t dyn[];
-  const int K1 = is_policy(LOSS) ? 1 : a.K + 1;
-  int* s_id = reinterpret_cast<int*>(dyn);           // sparse entries' vocabulary ids (-1: none)
-  float* s_u = reinterpret_cast<float*>(s_id + K1);  // teacher logits
-  float* s_c = s_u + K1;                             // coefficient subtracted at the entry
-  float* s_z = s_c + K1;                             // the student's logit there
-  __shared__ float4 rec[2][LOGIT_MAX_CLUSTER * WARPS];
-  __shared__ RowCoef coef;
-  __shared__ double dsum[WARPS];
+  constexpr int LANE_CHUNKS = TILE_CHUNKS / 32;
+  extern __shared__ __align__(128) uint8_t dyn_tiles[];
+  const int K1 = is_policy(LOSS) ? 0 : a.K + 1;
+  // the warps' rings, then twice (for two rows) the sparse entries: vocabulary
+  // ids (-1: none), coefficients subtracted there, the student's logits, the teacher's
+  int* entries = reinterpret_cast<int*>(dyn_tiles + LOGIT_RING_BYTES);
+  __shared__ float4 rec[2][LOGIT_MAX_CLUSTER * LOGIT_WARPS];
+  __shared__ RowCoef coefs[2];
+  __shared__ double dsum[LOGIT_WARPS];
+  __shared__ uint64_t bars[LOGIT_WARPS * TILE_STAGES];
+  __shared__ int abort_flag;
   __shared__ bool is_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cs = static_cast<int>(cluster_nctarank());
   const int rank = static_cast<int>(cluster_ctarank());
   const int clusters = gridDim.x / cs;
+  const uint64_t keep = l2_evict_last(), last = l2_evict_first();
+  uint4* ring = reinterpret_cast<uint4*>(dyn_tiles) + warp * (TILE_STAGES * TILE_CHUNKS);
+  const uint32_t bar0 = smem_u32(bars + warp * TILE_STAGES);
+  if (lane < TILE_STAGES) mbar_init(bar0 + 8u * lane, 1);
+  if (tid == 0) abort_flag = 0;
+  fence_mbar_init();
+  __syncthreads();
   const int n_valid = *a.n_valid;
   const double inv_n = n_valid > 0 ? 1.0 / static_cast<double>(n_valid) : 0.0;
-  const uint64_t once = l2_evict_first();
-  int parity = 0;
-  for (int row = blockIdx.x / cs; row < a.N; row += clusters) {
-    const T* z = static_cast<const T*>(a.z) + static_cast<long long>(row) * a.ld;
-    T* g = a.g ? static_cast<T*>(a.g) + static_cast<long long>(row) * a.ldg : nullptr;
-    // elements in front of the first 16-byte boundary, chunks, elements behind the last one
-    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T));
-    const int head = min(a.V, mis ? EPC - mis : 0);
-    const int chunks = (a.V - head) / EPC;
-    const int edges = a.V - chunks * EPC;
-    const int per = (chunks + cs - 1) / cs;
-    const int c0 = min(chunks, rank * per), c1 = min(chunks, c0 + per);
-    const T* zc = z + head;
-    // the gradient row shares the logits' alignment, or its elements are stored one by one
-    const bool vec_out = g && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
-    const int edge_col = rank == 0 && tid < edges ? (tid < head ? tid : a.V - edges + tid) : -1;
-    auto put = [&](int c, const uint4& o) {
-      if (vec_out) {
-        st_l2hint_v4(reinterpret_cast<uint4*>(g + head) + c, o, once);
-      } else {
-#pragma unroll
-        for (int e = 0; e < EPC; ++e) g[head + c * EPC + e] = reinterpret_cast<const T*>(&o)[e];
-      }
-    };
+  const int walks = a.g ? 2 : 1;
+  auto next_counting = [&](int r) {
+    while (r < a.N && !row_counts(a, a.y[r])) r += clusters;
+    return r;
+  };
 
+  // ---- the warp's ring: tiles are issued and used in the same order
+  const int first = blockIdx.x / cs;
+  int ahead = next_counting(first);  // row of the next tile to issue
+  RowPart<T> ap(a, min(ahead, a.N - 1), rank, cs, warp);
+  int ahead_k = 0;                   // its number in the row's 2 * tiles (or tiles) ones
+  int in_stage = 0;
+  auto issue = [&]() {
+    while (ahead < a.N && ahead_k == walks * ap.tiles) {
+      ahead = next_counting(ahead + clusters);
+      ahead_k = 0;
+      if (ahead < a.N) ap = RowPart<T>(a, ahead, rank, cs, warp);
+    }
+    if (ahead >= a.N || *const_cast<volatile int*>(&abort_flag)) return;
+    const bool again = ahead_k >= ap.tiles;
+    const int at = ap.tile_at(again ? 2 * ap.tiles - 1 - ahead_k : ahead_k, warp);
+    if (lane == 0) {
+      const uint32_t bytes = static_cast<uint32_t>(ap.tile_size(at)) * 16u;
+      mbar_arrive_expect_tx(bar0 + 8u * in_stage, bytes);
+      bulk_load(smem_u32(ring + in_stage * TILE_CHUNKS), reinterpret_cast<const uint4*>(ap.z + ap.col0) + at, bytes,
+                bar0 + 8u * in_stage, again || walks == 1 ? last : keep);
+    }
+    ++ahead_k;
+    if (++in_stage == TILE_STAGES) in_stage = 0;
+  };
+  int stage = 0;          // of the tile in use
+  uint32_t phase = 0;
+  bool freed_late = false;  // the last tile's stage is free once its gradient has been read out
+  auto arrived = [&]() {
+    if (freed_late) {
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+      issue();
+      freed_late = false;
+    }
+    if (!mbar_wait(bar0 + 8u * stage, phase, &abort_flag, a.timeout_ns)) {
+      *const_cast<volatile int*>(&abort_flag) = 1;
+      raise_status(a.status, ST_TIMEOUT);
+    }
+    __syncwarp();
+  };
+  auto advance = [&]() {
+    if (++stage == TILE_STAGES) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  };
+  for (int k = 0; k < TILE_STAGES; ++k) issue();
+
+  auto lifted = [&](float x) { return is_policy(LOSS) ? max_nan(x, LOGIT_LOWEST) : x; };
+  const float none = is_policy(LOSS) ? LOGIT_NONE : -INFINITY;
+  const uint64_t zs2 = f32x2(a.zs, a.zs), one2 = f32x2(LOG2E, LOG2E);
+  int parity = 0;
+  for (int row = first; row < a.N; row += clusters) {
+    const RowPart<T> p(a, row, rank, cs, warp);
+    const int edge_col = p.edge_col(a, rank, tid);
     const int y = a.y[row];
-    const bool in_range = y >= 0 && y < a.V;
-    if (y == a.ignore_index || !in_range) {
+    if (!row_counts(a, y)) {
       if (rank == 0 && tid == 0) {
         if (y != a.ignore_index) raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
         a.row_acc[row] = 0.0;
@@ -424,80 +509,89 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
           a.out_rows[row] = 0.f;
         }
       }
-      if (g) {
-        for (int c = c0 + tid; c < c1; c += THREADS) put(c, make_uint4(0u, 0u, 0u, 0u));
-        if (edge_col >= 0) g[edge_col] = L::round(0.f);
+      if (p.g) {
+        if ((reinterpret_cast<uintptr_t>(p.g + p.col0) & 15) == 0) {
+          uint4* gv = reinterpret_cast<uint4*>(p.g + p.col0);
+          for (int c = tid; c < p.n; c += LOGIT_THREADS) st_l2hint_v4(gv + c, make_uint4(0u, 0u, 0u, 0u), last);
+        } else {
+          for (int e = tid; e < p.n * EPC; e += LOGIT_THREADS) p.g[p.col0 + e] = L::round(0.f);
+        }
+        if (edge_col >= 0) p.g[edge_col] = L::round(0.f);
       }
       continue;
     }
 
-    // ---- the row's part of this CTA
-    const uint4* zt = reinterpret_cast<const uint4*>(zc) + (c0 + tid);
-    const int mine = c1 - c0 - tid;  // chunks from this thread's first on: u * THREADS < mine
-    uint4 raw[NCH];
-#pragma unroll
-    for (int u = 0; u < NCH; ++u)
-      raw[u] = u * THREADS < mine ? ld_l2hint_v4(zt + u * THREADS, once)
-                                  : make_uint4(L::NEG_INF, L::NEG_INF, L::NEG_INF, L::NEG_INF);
-    auto lifted = [&](float x) { return is_policy(LOSS) ? max_nan(x, LOGIT_LOWEST) : x; };
-    const float none = is_policy(LOSS) ? LOGIT_NONE : -INFINITY;
-    float edge = edge_col >= 0 ? L::load(z + edge_col) : -INFINITY;
+    // ---- what the row has besides its tiles, read ahead of its use
+    float edge = edge_col >= 0 ? L::load(p.z + edge_col) : -INFINITY;
     PolicyIn pin{};
-    if (is_policy(LOSS) && tid == 0) pin = policy_load(a.pol, row);
-    // the sparse entries: the teacher's, then the target
-    for (int k = tid; k < K1; k += THREADS) {
-      int id = y;
-      float u = -INFINITY;
-      if (k < K1 - 1) {
-        const size_t at = static_cast<size_t>(row) * a.K + k;
-        id = a.ids[at];
-        if (id >= a.V) {
-          raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
-          id = -1;
+    float zy = 0.f;
+    double scale = 1.0;
+    if (tid < 32) {
+      if (is_policy(LOSS)) pin = policy_load(a.pol, row);
+      zy = L::load(p.z + y);
+      scale = a.reduction == RED_MEAN ? inv_n
+              : a.reduction == RED_NONE && a.row_scale ? static_cast<double>(a.row_scale[row]) : 1.0;
+    }
+    int* s_id = entries + parity * 4 * K1;
+    float* s_c = reinterpret_cast<float*>(s_id + K1);
+    float *s_z = s_c + K1, *s_u = s_z + K1;
+    if constexpr (!is_policy(LOSS)) {  // the teacher's entries, then the target
+      for (int k = tid; k < K1; k += LOGIT_THREADS) {
+        int id = y;
+        float u = -INFINITY;
+        if (k < a.K) {
+          const size_t at = static_cast<size_t>(row) * a.K + k;
+          id = a.ids[at];
+          if (id >= a.V) {
+            raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
+            id = -1;
+          }
+          if (id >= 0) u = load_as_f32(a.u, a.u_dtype, at);
         }
-        if (id >= 0) u = load_as_f32(a.u, a.u_dtype, at);
+        s_id[k] = id < 0 ? -1 : id;
+        s_u[k] = u;
+        s_z[k] = id >= 0 && (rank == 0 || p.has(id)) ? L::load(p.z + id) : 0.f;
       }
-      s_id[k] = id < 0 ? -1 : id;
-      s_u[k] = u;
-      s_z[k] = id < 0 ? 0.f : L::load(z + id);
     }
 
-    // ---- statistics
-    float top = edge;  // this thread's largest logit as it stands
-    RowStat st{-FLT_MAX, 0.f, 0.f};
-    for (int c = c0 + NCH * THREADS + tid; c < c1; c += THREADS) {  // beyond the registers
-      const uint4 v = ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + c, l2_evict_normal());
+    // ---- first walk: maximum and sums, online, each lane under its own maximum
+    float top = edge;  // the largest logit as it stands
+    RowStat w{is_policy(LOSS) ? LOGIT_LOWEST : -FLT_MAX, 0.f, 0.f};
+    if (is_policy(LOSS)) edge = edge_col >= 0 ? lifted(edge) : none;
+    if (edge_col >= 0) stat_add<LOSS>(w, edge, a.zs);
+    uint64_t l2 = f32x2(w.l, 0.f), t2 = f32x2(w.t, 0.f);  // two partial sums each
+    for (int k = 0; k < p.tiles; ++k) {
+      const int size = p.tile_size(p.tile_at(k, warp));
+      arrived();
+      uint4 v[LANE_CHUNKS];
+      const uint4* tile = ring + stage * TILE_CHUNKS + lane;
 #pragma unroll
-      for (int i = 0; i < EPC / 2; ++i) {
-        float lo, hi;
-        f32x2_split(L::pair(v, i), lo, hi);
-        top = fmaxf(top, fmaxf(lo, hi));
-        stat_add<LOSS>(st, lifted(lo), a.zs);
-        stat_add<LOSS>(st, lifted(hi), a.zs);
+      for (int u = 0; u < LANE_CHUNKS; ++u)
+        if (u * 32 + lane < size) v[u] = tile[u * 32];
+      __syncwarp();
+      issue();  // the tile is in registers
+      advance();
+      typename L::Max vmax = L::max_init();
+#pragma unroll
+      for (int u = 0; u < LANE_CHUNKS; ++u)
+        if (u * 32 + lane < size) L::max_add(vmax, v[u]);
+      const float tile_top = L::max_get(vmax);
+      top = fmaxf(top, tile_top);
+      if (tile_top > w.m) {
+        const float d = (w.m - tile_top) * a.zs, f = ex2_approx(d);
+        const uint64_t f2 = f32x2(f, f);
+        if constexpr (is_policy(LOSS)) {
+          const float df = fmaxf(d, NEG_BIG);
+          t2 = mul2(f2, fma2(l2, f32x2(df, df), t2));
+        }
+        if constexpr (LOSS == LOSS_DISTILL2) {
+          const float f1 = ex2_approx((w.m - tile_top) * LOG2E);
+          t2 = mul2(t2, f32x2(f1, f1));
+        }
+        l2 = mul2(l2, f2);
+        w.m = tile_top;
       }
-    }
-    typename L::Max vmax = L::max_init();
-#pragma unroll
-    for (int u = 0; u < NCH; ++u) L::max_add(vmax, raw[u]);
-    top = fmaxf(top, L::max_get(vmax));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // -FLT_MAX, not -infinity, so that the differences below are never NaN for it
-    RowStat w{fmaxf(top, is_policy(LOSS) ? LOGIT_LOWEST : -FLT_MAX), 0.f, 0.f};
-    if constexpr (is_policy(LOSS)) {
-#pragma unroll
-      for (int u = 0; u < NCH; ++u) {
-        if (u * THREADS < mine)
-          L::clamp(raw[u]);
-        else
-          raw[u] = L::none();
-      }
-      edge = edge_col >= 0 ? lifted(edge) : none;
-    }
-    const uint64_t zs2 = f32x2(a.zs, a.zs), one2 = f32x2(LOG2E, LOG2E);
-    {
       const uint64_t neg_m2 = f32x2(-w.m, -w.m);
-      uint64_t l2 = 0ull, t2 = 0ull;  // two partial sums each
       auto fold = [&](uint64_t x) {
         const uint64_t d0 = add2(x, neg_m2);
         uint64_t d = mul2(d0, zs2);
@@ -517,136 +611,138 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
         }
       };
 #pragma unroll
-      for (int u = 0; u < NCH; ++u) {
+      for (int u = 0; u < LANE_CHUNKS; ++u) {
+        if (u * 32 + lane < size) {
+          if constexpr (is_policy(LOSS)) L::clamp(v[u]);
 #pragma unroll
-        for (int i = 0; i < EPC / 2; ++i) fold(L::pair(raw[u], i));
+          for (int i = 0; i < EPC / 2; ++i) fold(L::pair(v[u], i));
+        }
       }
-      fold(f32x2(edge, none));
+    }
+    // the lanes under the warp's maximum
+    {
       float lo, hi;
       f32x2_split(l2, lo, hi);
       w.l = lo + hi;
       f32x2_split(t2, lo, hi);
       w.t = lo + hi;
-    }
-    if (c1 - c0 > NCH * THREADS) stat_merge<LOSS>(w, st, a.zs);
+      RowStat o{w.m, 0.f, 0.f};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      w.l += __shfl_xor_sync(0xffffffffu, w.l, o);
-      w.t += __shfl_xor_sync(0xffffffffu, w.t, o);
+      for (int s = 16; s > 0; s >>= 1) {
+        o.m = fmaxf(o.m, __shfl_xor_sync(0xffffffffu, o.m, s));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      }
+      stat_merge<LOSS>(o, w, a.zs);
+      w = o;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) {
+        w.l += __shfl_xor_sync(0xffffffffu, w.l, s);
+        w.t += __shfl_xor_sync(0xffffffffu, w.t, s);
+      }
     }
     if (cs == 1) {
       if (lane == 0) rec[parity][warp] = make_float4(w.m, w.l, w.t, top);
       __syncthreads();
     } else {
       if (lane < cs)
-        st_cluster_f4(mapa_shared(smem_u32(&rec[parity][rank * WARPS + warp]), lane), make_float4(w.m, w.l, w.t, top));
+        st_cluster_f4(mapa_shared(smem_u32(&rec[parity][rank * LOGIT_WARPS + warp]), lane),
+                      make_float4(w.m, w.l, w.t, top));
       cluster_sync_all();
     }
 
-    // ---- the row's totals (every warp, the same order everywhere)
-    const int records = cs * WARPS;
-    w.m = -FLT_MAX;
-    for (int r = lane; r < records; r += 32) w.m = fmaxf(w.m, rec[parity][r].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) w.m = fmaxf(w.m, __shfl_xor_sync(0xffffffffu, w.m, o));
+    // ---- the row's totals and scalars
     if (warp == 0) {
-      w.l = w.t = 0.f;
+      const int records = cs * LOGIT_WARPS;
+      w = RowStat{-FLT_MAX, 0.f, 0.f};
       top = -INFINITY;
       for (int r = lane; r < records; r += 32) {
         const float4 v = rec[parity][r];
+        stat_merge<LOSS>(w, RowStat{v.x, v.y, v.z}, a.zs);
         top = fmaxf(top, v.w);
-        RowStat o{w.m, 0.f, 0.f};
-        stat_merge<LOSS>(o, RowStat{v.x, v.y, v.z}, a.zs);
-        w.l += o.l;
-        w.t += o.t;
       }
+      RowStat o{w.m, 0.f, 0.f};
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        w.l += __shfl_xor_sync(0xffffffffu, w.l, o);
-        w.t += __shfl_xor_sync(0xffffffffu, w.t, o);
+      for (int s = 16; s > 0; s >>= 1) o.m = fmaxf(o.m, __shfl_xor_sync(0xffffffffu, o.m, s));
+      stat_merge<LOSS>(o, w, a.zs);
+      w = o;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) {
+        w.l += __shfl_xor_sync(0xffffffffu, w.l, s);
+        w.t += __shfl_xor_sync(0xffffffffu, w.t, s);
       }
       if (is_policy(LOSS) && !__any_sync(0xffffffffu, top > -INFINITY)) w.l = 0.f;  // every logit is -infinity: NaN
       // Log-probabilities as (z - m)/T - ln L: the difference first, so that a
       // row whose every logit is the type's lowest value still has one.
       const double m = static_cast<double>(w.m);
       const double lnL = log(static_cast<double>(w.l));
-      const double s = a.reduction == RED_MEAN ? inv_n
-                       : a.reduction == RED_NONE && a.row_scale ? static_cast<double>(a.row_scale[row]) : 1.0;
+      const double inv_l = 1.0 / static_cast<double>(w.l);
       double total = 0.0;
+      RowCoef c{w.m, 0.f, 0.f, 0.f, 0.f};
       if constexpr (is_policy(LOSS)) {
-        if (lane == 0) {
-          const float zy = s_z[0] == -INFINITY ? s_z[0] : lifted(s_z[0]);
-          const double lp = (static_cast<double>(zy) - m) * a.inv_T - lnL;
-          const double inv_l = 1.0 / static_cast<double>(w.l);
-          const double H = lnL - static_cast<double>(w.t) * inv_l * LN2;
-          const PolicyRow p = policy_row(a.pol, pin, lp);
-          total = p.loss;
-          double a0 = -p.dlogp, a1 = 0.0;
-          if (a.ent_coef != 0.0) {
-            total -= a.ent_coef * H;
-            a0 += a.ent_coef * (H - lnL);
-            a1 = a.ent_coef * LN2;
-          }
-          const double f = s * a.inv_T;
-          s_c[0] = static_cast<float>(-p.dlogp * f);
-          coef.a = static_cast<float>(a0 * f * inv_l);
-          coef.b = static_cast<float>(a1 * f * inv_l);
-          if (rank == 0) {
-            a.out_logp[row] = static_cast<float>(lp);
-            a.out_entropy[row] = static_cast<float>(H);
-            a.out_kl[row] = static_cast<float>(p.kl);
-          }
+        const double lp = (static_cast<double>(zy == -INFINITY ? zy : lifted(zy)) - m) * a.inv_T - lnL;
+        const double H = lnL - static_cast<double>(w.t) * inv_l * LN2;
+        const PolicyRow r = policy_row(a.pol, pin, lp);
+        total = r.loss;
+        double a0 = -r.dlogp, a1 = 0.0;
+        if (a.ent_coef != 0.0) {
+          total -= a.ent_coef * H;
+          a0 += a.ent_coef * (H - lnL);
+          a1 = a.ent_coef * LN2;
+        }
+        const double f = scale * a.inv_T;
+        c.a = static_cast<float>(a0 * f * inv_l);
+        c.b = static_cast<float>(a1 * f * inv_l);
+        c.c = static_cast<float>(-r.dlogp * f);
+        c.zy = lifted(zy);
+        if (rank == 0 && lane == 0) {
+          a.out_logp[row] = static_cast<float>(lp);
+          a.out_entropy[row] = static_cast<float>(H);
+          a.out_kl[row] = static_cast<float>(r.kl);
         }
       } else {
         const TeacherShift ts = teacher_shift(s_u, a.K, lane, a.inv_T, a.teacher_lse, row);
         double Q = 0.0, kl = 0.0;
-        if (ts.any) {
-          for (int k = lane; k < a.K; k += 32) {
-            const double lq = static_cast<double>(s_u[k]) * a.inv_T - ts.shift;
-            const float q = expf(static_cast<float>(lq));
-            s_c[k] = static_cast<float>(static_cast<double>(q) * a.kd * a.inv_T * s);
-            Q += q;
-            if (!(q == 0.f)) kl += static_cast<double>(q) * (lq - ((static_cast<double>(s_z[k]) - m) * a.inv_T - lnL));
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            Q += __shfl_xor_sync(0xffffffffu, Q, o);
-            kl += __shfl_xor_sync(0xffffffffu, kl, o);
-          }
-        } else {
-          for (int k = lane; k < a.K; k += 32) s_c[k] = 0.f;
+        for (int k = lane; k < a.K; k += 32) {
+          const double lq = static_cast<double>(s_u[k]) * a.inv_T - ts.shift;
+          const float q = ts.any ? expf(static_cast<float>(lq)) : 0.f;
+          s_c[k] = static_cast<float>(static_cast<double>(q) * a.kd * a.inv_T * scale);
+          Q += q;
+          if (rank == 0 && !(q == 0.f))
+            kl += static_cast<double>(q) * (lq - ((static_cast<double>(s_z[k]) - m) * a.inv_T - lnL));
         }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) {
+          Q += __shfl_xor_sync(0xffffffffu, Q, s);
+          kl += __shfl_xor_sync(0xffffffffu, kl, s);
+        }
+        if (a.kd != 0.0) total = a.kd * kl;
+        double da = a.kd * Q * a.inv_T, db = 0.0;
+        if (a.ce != 0.0) {
+          const double ln1 = LOSS == LOSS_DISTILL2 ? log(static_cast<double>(w.t)) : lnL;
+          total += a.ce * (m - static_cast<double>(zy) + ln1);
+          if constexpr (LOSS == LOSS_DISTILL2)
+            db = a.ce / static_cast<double>(w.t);
+          else
+            da += a.ce;
+        }
+        c.a = static_cast<float>(da * scale * inv_l);
+        c.b = static_cast<float>(db * scale);
         if (lane == 0) {
-          if (a.kd != 0.0) total = a.kd * kl;
-          double da = a.kd * Q * a.inv_T, db = 0.0;
-          if (a.ce != 0.0) {
-            const double ln1 = LOSS == LOSS_DISTILL2 ? log(static_cast<double>(w.t)) : lnL;
-            total += a.ce * (m - static_cast<double>(s_z[a.K]) + ln1);
-            if constexpr (LOSS == LOSS_DISTILL2)
-              db = a.ce / static_cast<double>(w.t);
-            else
-              da += a.ce;
-          }
-          s_c[a.K] = static_cast<float>(a.ce * s);
-          coef.a = static_cast<float>(da * s / static_cast<double>(w.l));
-          coef.b = static_cast<float>(db * s);
+          s_c[a.K] = static_cast<float>(a.ce * scale);
           if (rank == 0 && a.out_rows) a.out_rows[row] = static_cast<float>(total);
         }
       }
-      if (rank == 0 && lane == 0) a.row_acc[row] = a.reduction == RED_MEAN ? total : total * s;
+      if (lane == 0) {
+        coefs[parity] = c;
+        if (rank == 0) a.row_acc[row] = a.reduction == RED_MEAN ? total : total * scale;
+      }
     }
-    __syncthreads();
 
-    // ---- the gradient
-    if (g) {
-      // Unpack the chunks anew here: values kept unpacked since the sums would
-      // take twice the registers, and spill.
-#pragma unroll
-      for (int u = 0; u < NCH; ++u)
-        asm volatile("" : "+r"(raw[u].x), "+r"(raw[u].y), "+r"(raw[u].z), "+r"(raw[u].w));
-      const RowCoef c = coef;
-      const float m = w.m;
-      const uint64_t neg_m2 = f32x2(-m, -m), a2 = f32x2(c.a, c.a), b2 = f32x2(c.b, c.b);
+    // ---- second walk, backwards: the gradient
+    if (a.g) {
+      __syncthreads();
+      const RowCoef c = coefs[parity];
+      const uint64_t neg_m2 = f32x2(-c.m, -c.m), a2 = f32x2(c.a, c.a), b2 = f32x2(c.b, c.b);
       auto dense2 = [&](uint64_t x) {
         const uint64_t d0 = add2(x, neg_m2);
         uint64_t d = mul2(d0, zs2);
@@ -670,49 +766,75 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
         f32x2_split(dense2(f32x2(x, x)), lo, hi);
         return lo;
       };
-      auto grad_chunk = [&](const uint4& v) {
-        uint4 o;
-#pragma unroll
-        for (int i = 0; i < EPC / 2; ++i) {
-          float lo, hi;
-          f32x2_split(dense2(L::pair(v, i)), lo, hi);
-          L::put(o, i, lo, hi);
-        }
-        return o;
+      // what is subtracted at column id: equal ids add up, and each writes the same sum
+      auto sparse = [&](int id) {
+        if (is_policy(LOSS)) return id == y ? c.c : 0.f;
+        float sum = 0.f;
+        for (int k = 0; k < K1; ++k)
+          if (s_id[k] == id) sum += s_c[k];
+        return sum;
       };
-      if (vec_out) {
-        uint4* gt = reinterpret_cast<uint4*>(g + head) + (c0 + tid);
+      if (edge_col >= 0) p.g[edge_col] = L::round(dense(edge) - sparse(edge_col));
+      for (int k = p.tiles - 1; k >= 0; --k) {
+        const int at = p.tile_at(k, warp), size = p.tile_size(at);
+        const int col = p.col0 + at * EPC, end = col + size * EPC;
+        arrived();
+        uint4* tile = ring + stage * TILE_CHUNKS;
 #pragma unroll
-        for (int u = 0; u < NCH; ++u)
-          if (u * THREADS < mine) st_l2hint_v4(gt + u * THREADS, grad_chunk(raw[u]), once);
-      } else {
+        for (int u = 0; u < LANE_CHUNKS; ++u) {
+          if (u * 32 + lane < size) {
+            uint4 v = tile[u * 32 + lane], o;
+            if constexpr (is_policy(LOSS)) L::clamp(v);
 #pragma unroll
-        for (int u = 0; u < NCH; ++u)
-          if (u * THREADS < mine) put(c0 + u * THREADS + tid, grad_chunk(raw[u]));
-      }
-      for (int ch = c0 + NCH * THREADS + tid; ch < c1; ch += THREADS) {
-        uint4 v = ld_l2hint_v4(reinterpret_cast<const uint4*>(zc) + ch, once);
-        if constexpr (is_policy(LOSS)) L::clamp(v);
-        put(ch, grad_chunk(v));
-      }
-      if (edge_col >= 0) g[edge_col] = L::round(dense(edge));
-      __syncthreads();
-      // The sparse entries of this CTA's part; equal ids add up, and each of
-      // them writes the same sum.
-      const int lo = head + c0 * EPC, hi = head + c1 * EPC;
-      for (int k = tid; k < K1; k += THREADS) {
-        const int id = s_id[k];
-        const bool mine = id >= lo && id < hi ? true : rank == 0 && id >= 0 && (id < head || id >= head + chunks * EPC);
-        if (!mine) continue;
-        float c_sum = 0.f;
-        for (int i = 0; i < K1; ++i)
-          if (s_id[i] == id) c_sum += s_c[i];
-        g[id] = L::round(dense(lifted(s_z[k])) - c_sum);
+            for (int i = 0; i < EPC / 2; ++i) {
+              float lo, hi;
+              f32x2_split(dense2(L::pair(v, i)), lo, hi);
+              L::put(o, i, lo, hi);
+            }
+            tile[u * 32 + lane] = o;
+          }
+        }
+        if constexpr (is_policy(LOSS)) {
+          if (y >= col && y < end) {
+            __syncwarp();
+            if (lane == 0) reinterpret_cast<T*>(tile)[y - col] = L::round(dense(c.zy) - c.c);
+          }
+        } else {
+          __syncwarp();
+          for (int i = lane; i < K1; i += 32) {
+            const int id = s_id[i];
+            if (id >= col && id < end) reinterpret_cast<T*>(tile)[id - col] = L::round(dense(s_z[i]) - sparse(id));
+          }
+        }
+        if (p.vec_out) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            bulk_store(p.g + col, smem_u32(tile), static_cast<uint32_t>(size) * 16u, last);
+            bulk_commit();
+          }
+          freed_late = true;
+        } else {
+          __syncwarp();
+          for (int e = lane; e < size * EPC; e += 32) p.g[col + e] = reinterpret_cast<const T*>(tile)[e];
+          fence_proxy_async_smem();
+          __syncwarp();
+          issue();
+        }
+        advance();
       }
     }
-    __syncthreads();  // the shared row data is reused
     parity ^= 1;
   }
+  if (lane == 0) {
+    if (*const_cast<volatile int*>(&abort_flag)) {  // a late copy must not outlive the CTA (again with a limit)
+      int no = 0;
+      for (int k = 0; k < TILE_STAGES; ++k) mbar_wait(bar0 + 8u * k, phase ^ (k < stage ? 1u : 0u), &no, a.timeout_ns);
+    }
+    bulk_wait_read<0>();
+  }
+  __syncwarp();
+  if (cs > 1) cluster_sync_all();  // no CTA leaves while another may still write a record into it
   // the loss, by the last cluster to finish
   if (rank != 0) return;
   if (tid == 0) {
@@ -722,7 +844,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) flce_logit_loss_kerne
   __syncthreads();
   if (!is_last) return;
   __threadfence();
-  const double t = ordered_sum<THREADS>(a.row_acc, a.N, dsum);
+  const double t = ordered_sum<LOGIT_THREADS>(a.row_acc, a.N, dsum);
   if (tid == 0) *a.loss = static_cast<float>(a.reduction == RED_MEAN ? t * inv_n : t);
 }
 
