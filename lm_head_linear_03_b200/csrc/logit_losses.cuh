@@ -340,6 +340,11 @@ struct RowCoef {
   float c, zy;   // policy: subtracted at the target, and the logit there
 };
 
+template <bool B>
+struct Flag {  // a compile-time truth value to pass to a lambda
+  static constexpr bool value = B;
+};
+
 constexpr int LOGIT_THREADS = 256;
 constexpr int LOGIT_WARPS = LOGIT_THREADS / 32;
 constexpr int LOGIT_MAX_CLUSTER = 8;
@@ -560,21 +565,20 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
     if (is_policy(LOSS)) edge = edge_col >= 0 ? lifted(edge) : none;
     if (edge_col >= 0) stat_add<LOSS>(w, edge, a.zs);
     uint64_t l2 = f32x2(w.l, 0.f), t2 = f32x2(w.t, 0.f);  // two partial sums each
-    for (int k = 0; k < p.tiles; ++k) {
-      const int size = p.tile_size(p.tile_at(k, warp));
-      arrived();
+    auto fold_tile = [&](auto full, int size) {
+      auto has = [&](int u) { return decltype(full)::value || u * 32 + lane < size; };
       uint4 v[LANE_CHUNKS];
       const uint4* tile = ring + stage * TILE_CHUNKS + lane;
 #pragma unroll
       for (int u = 0; u < LANE_CHUNKS; ++u)
-        if (u * 32 + lane < size) v[u] = tile[u * 32];
+        if (has(u)) v[u] = tile[u * 32];
       __syncwarp();
       issue();  // the tile is in registers
       advance();
       typename L::Max vmax = L::max_init();
 #pragma unroll
       for (int u = 0; u < LANE_CHUNKS; ++u)
-        if (u * 32 + lane < size) L::max_add(vmax, v[u]);
+        if (has(u)) L::max_add(vmax, v[u]);
       const float tile_top = L::max_get(vmax);
       top = fmaxf(top, tile_top);
       if (tile_top > w.m) {
@@ -612,12 +616,20 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
       };
 #pragma unroll
       for (int u = 0; u < LANE_CHUNKS; ++u) {
-        if (u * 32 + lane < size) {
+        if (has(u)) {
           if constexpr (is_policy(LOSS)) L::clamp(v[u]);
 #pragma unroll
           for (int i = 0; i < EPC / 2; ++i) fold(L::pair(v[u], i));
         }
       }
+    };
+    for (int k = 0; k < p.tiles; ++k) {
+      const int size = p.tile_size(p.tile_at(k, warp));
+      arrived();
+      if (size == TILE_CHUNKS)
+        fold_tile(Flag<true>{}, size);
+      else
+        fold_tile(Flag<false>{}, size);
     }
     // the lanes under the warp's maximum
     {
@@ -780,9 +792,10 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
         const int col = p.col0 + at * EPC, end = col + size * EPC;
         arrived();
         uint4* tile = ring + stage * TILE_CHUNKS;
+        auto write_tile = [&](auto full) {
 #pragma unroll
         for (int u = 0; u < LANE_CHUNKS; ++u) {
-          if (u * 32 + lane < size) {
+          if (decltype(full)::value || u * 32 + lane < size) {
             uint4 v = tile[u * 32 + lane], o;
             if constexpr (is_policy(LOSS)) L::clamp(v);
 #pragma unroll
@@ -794,6 +807,11 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
             tile[u * 32 + lane] = o;
           }
         }
+        };
+        if (size == TILE_CHUNKS)
+          write_tile(Flag<true>{});
+        else
+          write_tile(Flag<false>{});
         if constexpr (is_policy(LOSS)) {
           if (y >= col && y < end) {
             __syncwarp();
