@@ -339,8 +339,10 @@ typedef enum { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_FP16 = 1, FLCE_DTYPE_FP32 = 2 } f
  * clip_low in [0, 1], clip_high >= 0 (infinity: no upper border); kl_coef
  * finite, and 0 when d_ref_logp is NULL.  All pointers DEVICE: fp32 [N] inputs
  * and outputs, y int32 [N], d_loss fp64 [1], d_status int32 [1]; workspace of
- * flce_ce_workspace_size(N, 1) bytes, 256-byte aligned.  Asynchronous; the
- * sums are fp64 in a fixed order. */
+ * flce_ce_workspace_size(N, 1) bytes, 256-byte aligned, or NULL for up to
+ * FLCE_CLIPPED_POLICY_NO_WORKSPACE rows (one block does those alone).
+ * Asynchronous; the sums are fp64 in a fixed order. */
+#define FLCE_CLIPPED_POLICY_NO_WORKSPACE 2048
 flce_status_t flce_clipped_policy(const float* d_row_loss, const int32_t* y, int64_t N, int32_t ignore_index,
                                   const float* d_old_logp, const float* d_advantage, const float* d_ref_logp,
                                   double clip_low, double clip_high, double kl_coef, int32_t reduction,

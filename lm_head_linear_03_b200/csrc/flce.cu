@@ -850,28 +850,19 @@ flce_status_t check_logits(const void* logits, int32_t dtype, int64_t ld, int64_
   return FLCE_OK;
 }
 
-// Rows up to which one CTA counts the valid ones.
-constexpr int64_t BEGIN_MAX_ROWS = 32768;
-
-// Zeroes the call's counters and status and counts its valid rows into the
-// control block of a ce_ws_layout workspace.
+// First launch of a call on per-row data (see flce_begin_kernel); its words lie
+// in the control block and the per-tile counts of a ce_ws_layout workspace.
 flce_status_t begin_rows(const int32_t* y, int64_t N, int32_t ignore_index, uint8_t* ws, const CeLayout& L,
-                         int32_t* d_status, cudaStream_t stream) {
-  unsigned int* ticket = reinterpret_cast<unsigned int*>(ws + L.ctrl + 4);
-  int* n_valid = reinterpret_cast<int*>(ws + L.ctrl + 8);
+                         int32_t* d_status, RowCounts* valid, unsigned int** ticket, cudaStream_t stream) {
+  *ticket = reinterpret_cast<unsigned int*>(ws + L.ctrl + 4);
+  int* counts = reinterpret_cast<int*>(ws + L.tile_valid);
+  const int64_t per = std::max<int64_t>(BEGIN_ROWS, (N + BEGIN_BLOCKS - 1) / BEGIN_BLOCKS);
+  const int blocks = static_cast<int>((N + per - 1) / per);
+  *valid = {counts, blocks};
   size_t slot;
-  if (N <= BEGIN_MAX_ROWS) {
-    prof_begin(stream, KIND_PREP, &slot);
-    flce_begin_kernel<<<1, BEGIN_THREADS, 0, stream>>>(y, static_cast<int>(N), ignore_index, ticket, n_valid,
-                                                       d_status);
-  } else {
-    if (cudaMemsetAsync(ws + L.ctrl, 0, 256, stream) != cudaSuccess ||
-        cudaMemsetAsync(d_status, 0, sizeof(int32_t), stream) != cudaSuccess)
-      return cuda_fail(__LINE__);
-    prof_begin(stream, KIND_PREP, &slot);
-    flce_prep_kernel<<<static_cast<int>((N + CM - 1) / CM), CM, 0, stream>>>(y, static_cast<int>(N), ignore_index,
-                                                                           nullptr, n_valid);
-  }
+  prof_begin(stream, KIND_PREP, &slot);
+  flce_begin_kernel<<<blocks, BEGIN_THREADS, 0, stream>>>(y, static_cast<int>(N), ignore_index, static_cast<int>(per),
+                                                          *ticket, counts, d_status);
   prof_end(stream, slot);
   return cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
 }
@@ -949,10 +940,8 @@ flce_status_t enqueue_logit_loss(LogitArgs& a, int loss, int32_t dtype, uint8_t*
   if (device_info(&di, &dev) != cudaSuccess) return cuda_fail(__LINE__);
   if (!di.sm100) return FLCE_ERR_UNSUPPORTED;
   const CeLayout L = ce_ws_layout(a.N);
-  const flce_status_t s = begin_rows(a.y, a.N, a.ignore_index, ws, L, a.status, stream);
+  const flce_status_t s = begin_rows(a.y, a.N, a.ignore_index, ws, L, a.status, &a.valid, &a.ticket, stream);
   if (s != FLCE_OK) return s;
-  a.ticket = reinterpret_cast<unsigned int*>(ws + L.ctrl + 4);
-  a.n_valid = reinterpret_cast<const int*>(ws + L.ctrl + 8);
   a.row_acc = reinterpret_cast<double*>(ws + L.row_acc);
   a.timeout_ns = DEFAULT_TIMEOUT_NS;
   const size_t smem = is_policy(loss) ? 0 : 2 * 16 * (static_cast<size_t>(a.K) + 1);
@@ -1178,7 +1167,7 @@ flce_status_t flce_clipped_policy(const float* d_row_loss, const int32_t* y, int
                                   float* d_row_weight, int32_t* d_status, void* workspace, size_t workspace_bytes,
                                   cudaStream_t stream) {
   if (!d_row_loss || !y || !d_advantage || !d_loss || !d_policy_loss || !d_kl || !d_row_weight || !d_status ||
-      !workspace || N <= 0 || N > (1ll << 30))
+      N <= 0 || N > (1ll << 30) || (!workspace && N > FLCE_CLIPPED_POLICY_NO_WORKSPACE))
     return FLCE_ERR_INVALID_ARGUMENT;
   flce_status_t s = check_reduction(reduction);
   if (s == FLCE_OK) s = check_policy(clip_low, clip_high, kl_coef, d_ref_logp);
@@ -1191,15 +1180,19 @@ flce_status_t flce_clipped_policy(const float* d_row_loss, const int32_t* y, int
     if (!aligned(p, 4)) return FLCE_ERR_UNSUPPORTED;
   if (!aligned(d_loss, 8) || !aligned(workspace, 256)) return FLCE_ERR_UNSUPPORTED;
   const CeLayout L = ce_ws_layout(N);
-  if (workspace_bytes < L.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  const bool one = N <= FLCE_CLIPPED_POLICY_NO_WORKSPACE;
+  if (!one && workspace_bytes < L.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   DevInfo di;
   int dev;
   if (device_info(&di, &dev) != cudaSuccess) return cuda_fail(__LINE__);
   if (!di.sm100) return FLCE_ERR_UNSUPPORTED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  s = begin_rows(y, N, ignore_index, ws, L, d_status, stream);
-  if (s != FLCE_OK) return s;
   PolicyRowsArgs a{};
+  if (!one) {
+    s = begin_rows(y, N, ignore_index, ws, L, d_status, &a.valid, &a.ticket, stream);
+    if (s != FLCE_OK) return s;
+    a.blk_sum = reinterpret_cast<double*>(ws + L.row_acc);
+  }
   a.pol = policy_args(d_old_logp, d_advantage, d_ref_logp, clip_low, clip_high, kl_coef);
   a.row_loss = d_row_loss;
   a.y = y;
@@ -1207,18 +1200,19 @@ flce_status_t flce_clipped_policy(const float* d_row_loss, const int32_t* y, int
   a.ignore_index = ignore_index;
   a.reduction = reduction;
   a.row_scale = reduction == FLCE_REDUCTION_NONE ? d_row_scale : nullptr;
-  a.n_valid = reinterpret_cast<const int*>(ws + L.ctrl + 8);
-  a.ticket = reinterpret_cast<unsigned int*>(ws + L.ctrl + 4);
-  a.blk_sum = reinterpret_cast<double*>(ws + L.row_acc);
   a.loss = d_loss;
+  a.status = d_status;
   a.out_rows = d_policy_loss;
   a.out_kl = d_kl;
   a.out_weight = d_row_weight;
-  const int grid = static_cast<int>(
-      std::min<int64_t>((N + POLICY_THREADS - 1) / POLICY_THREADS, static_cast<int64_t>(di.num_sms) * 8));
+  const int64_t blocks = (N + POLICY_THREADS * POLICY_ROWS - 1) / (POLICY_THREADS * POLICY_ROWS);
+  const int grid = static_cast<int>(std::min<int64_t>(blocks, static_cast<int64_t>(di.num_sms) * 8));
   size_t slot;
   prof_begin(stream, KIND_POLICY_ROWS, &slot);
-  flce_policy_rows_kernel<<<grid, POLICY_THREADS, 0, stream>>>(a);
+  if (one)
+    flce_policy_rows_kernel<true><<<1, POLICY_THREADS, 0, stream>>>(a);
+  else
+    flce_policy_rows_kernel<false><<<grid, POLICY_THREADS, 0, stream>>>(a);
   prof_end(stream, slot);
   return cudaGetLastError() == cudaSuccess ? FLCE_OK : cuda_fail(__LINE__);
 }

@@ -129,13 +129,18 @@ __device__ __forceinline__ float load_as_f32(const void* p, int dtype, size_t i)
 
 // ------------------------------------------------------------ setup, sums --
 
-// Counters and the status word of a call, and its number of valid rows
-// (one CTA: short enough for the row counts it is launched for).
-constexpr int BEGIN_THREADS = 1024;
+// The first launch of a call: sets its ticket and status word, and counts the
+// valid rows of each block's range.  The next launch adds the blocks' counts
+// (count_rows), so nothing has to be zeroed ahead.
+constexpr int BEGIN_THREADS = 512;
+constexpr int BEGIN_ROWS = 16 * BEGIN_THREADS;  // per block; more when that would take over BEGIN_BLOCKS blocks
+constexpr int BEGIN_BLOCKS = 256;
 __global__ void __launch_bounds__(BEGIN_THREADS)
-    flce_begin_kernel(const int32_t* y, int N, int ignore_index, unsigned int* ticket, int* n_valid, int* status) {
+    flce_begin_kernel(const int32_t* y, int N, int ignore_index, int per, unsigned int* ticket, int* counts, int* status) {
+  const int lo = blockIdx.x * per, hi = min(N, lo + per);
   int c = 0;
-  for (int i = threadIdx.x; i < N; i += BEGIN_THREADS) c += y[i] != ignore_index ? 1 : 0;
+#pragma unroll 4
+  for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += BEGIN_THREADS) c += y[i] != ignore_index ? 1 : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) c += __shfl_down_sync(0xffffffffu, c, o);
   __shared__ int w[BEGIN_THREADS / 32];
@@ -144,10 +149,25 @@ __global__ void __launch_bounds__(BEGIN_THREADS)
   if (threadIdx.x == 0) {
     int t = 0;
     for (int k = 0; k < BEGIN_THREADS / 32; ++k) t += w[k];
-    *n_valid = t;
-    *ticket = 0u;
-    *status = 0;
+    counts[blockIdx.x] = t;
+    if (blockIdx.x == 0) {
+      *ticket = 0u;
+      *status = 0;
+    }
   }
+}
+
+// The valid rows of the call, from the first launch's counts (every warp for itself).
+struct RowCounts {
+  const int* counts;
+  int blocks;
+};
+__device__ __forceinline__ int count_rows(const RowCounts& r) {
+  int n = 0;
+  for (int i = threadIdx.x & 31; i < r.blocks; i += 32) n += r.counts[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
 }
 
 // The last block to finish adds the rows' contributions in row order: a fixed
@@ -155,6 +175,7 @@ __global__ void __launch_bounds__(BEGIN_THREADS)
 template <int THREADS>
 __device__ __forceinline__ double ordered_sum(const double* v, int n, double* scratch) {
   double s = 0.0;
+#pragma unroll 8
   for (int i = threadIdx.x; i < n; i += THREADS) s += __ldcg(v + i);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(0xffffffffu, s, o);
@@ -209,37 +230,89 @@ struct PolicyRowsArgs {
   const int32_t* y;
   int N, ignore_index, reduction;
   const float* row_scale;
-  const int* n_valid;
+  RowCounts valid;      // several blocks: the first launch's counts
   unsigned int* ticket;
   double* blk_sum;      // [gridDim.x]
   double* loss;
+  int* status;
   float* out_rows;      // [N] policy loss per row
   float* out_kl;        // [N]
   float* out_weight;    // [N] s_i dL_i/dl_i
 };
 
+// A thread takes four neighbouring rows, so that the loads of each of its up to
+// six streams are one 16-byte access where the stream allows it.
 constexpr int POLICY_THREADS = 256;
-__global__ void __launch_bounds__(POLICY_THREADS) flce_policy_rows_kernel(const PolicyRowsArgs a) {
-  const int n = *a.n_valid;
-  const double inv_n = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
-  double acc = 0.0;
-  for (int i = blockIdx.x * POLICY_THREADS + threadIdx.x; i < a.N; i += gridDim.x * POLICY_THREADS) {
-    float rows = 0.f, kl = 0.f, weight = 0.f;
-    if (a.y[i] != a.ignore_index) {
-      const PolicyRow p = policy_row(a.pol, policy_load(a.pol, i), -static_cast<double>(a.row_loss[i]));
-      const double s = a.reduction == RED_MEAN ? inv_n
-                       : a.reduction == RED_NONE && a.row_scale ? static_cast<double>(a.row_scale[i]) : 1.0;
-      rows = static_cast<float>(p.loss);
-      kl = static_cast<float>(p.kl);
-      weight = static_cast<float>(-p.dlogp * s);
-      acc += a.reduction == RED_MEAN ? p.loss : p.loss * s;
-    }
-    a.out_rows[i] = rows;
-    a.out_kl[i] = kl;
-    a.out_weight[i] = weight;
+constexpr int POLICY_ROWS = 4;
+
+__device__ __forceinline__ void load_rows4(const float* p, int i, int n, float (&v)[POLICY_ROWS]) {
+  if (!p) return;
+  if (n == POLICY_ROWS && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    const float4 t = *reinterpret_cast<const float4*>(p + i);
+    v[0] = t.x;
+    v[1] = t.y;
+    v[2] = t.z;
+    v[3] = t.w;
+  } else {
+    for (int k = 0; k < n; ++k) v[k] = p[i + k];
   }
+}
+__device__ __forceinline__ void store_rows4(float* p, int i, int n, const float (&v)[POLICY_ROWS]) {
+  if (n == POLICY_ROWS && (reinterpret_cast<uintptr_t>(p) & 15) == 0)
+    *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    for (int k = 0; k < n; ++k) p[i + k] = v[k];
+}
+
+// ONE: a single block, which counts the valid rows itself; its only launch.
+// Otherwise the last block to finish adds the blocks' sums in order.
+template <bool ONE>
+__global__ void __launch_bounds__(POLICY_THREADS) flce_policy_rows_kernel(const PolicyRowsArgs a) {
   __shared__ double w[POLICY_THREADS / 32];
   __shared__ bool is_last;
+  int n_valid;
+  if constexpr (ONE) {
+    int c = 0;
+    for (int i0 = 0; i0 < a.N; i0 += POLICY_THREADS) {
+      const int i = i0 + static_cast<int>(threadIdx.x);
+      c += __syncthreads_count(i < a.N && a.y[i] != a.ignore_index);
+    }
+    n_valid = c;
+  } else {
+    n_valid = count_rows(a.valid);
+  }
+  const double inv_n = n_valid > 0 ? 1.0 / static_cast<double>(n_valid) : 0.0;
+  double acc = 0.0;
+  for (int i = (blockIdx.x * POLICY_THREADS + threadIdx.x) * POLICY_ROWS; i < a.N;
+       i += gridDim.x * (POLICY_THREADS * POLICY_ROWS)) {
+    const int n = min(POLICY_ROWS, a.N - i);
+    float l[POLICY_ROWS], yf[POLICY_ROWS], scale[POLICY_ROWS];
+    PolicyIn in[POLICY_ROWS];
+    float old[POLICY_ROWS] = {}, adv[POLICY_ROWS] = {}, ref[POLICY_ROWS] = {};
+    load_rows4(reinterpret_cast<const float*>(a.y), i, n, yf);
+    load_rows4(a.row_loss, i, n, l);
+    load_rows4(a.pol.old_logp, i, n, old);
+    load_rows4(a.pol.adv, i, n, adv);
+    load_rows4(a.pol.ref_logp, i, n, ref);
+    load_rows4(a.row_scale, i, n, scale);
+    float rows[POLICY_ROWS] = {}, kl[POLICY_ROWS] = {}, weight[POLICY_ROWS] = {};
+#pragma unroll
+    for (int k = 0; k < POLICY_ROWS; ++k) {
+      if (k < n && __float_as_int(yf[k]) != a.ignore_index) {
+        in[k] = {old[k], adv[k], ref[k]};
+        const PolicyRow p = policy_row(a.pol, in[k], -static_cast<double>(l[k]));
+        const double s = a.reduction == RED_MEAN ? inv_n
+                         : a.reduction == RED_NONE && a.row_scale ? static_cast<double>(scale[k]) : 1.0;
+        rows[k] = static_cast<float>(p.loss);
+        kl[k] = static_cast<float>(p.kl);
+        weight[k] = static_cast<float>(-p.dlogp * s);
+        acc += a.reduction == RED_MEAN ? p.loss : p.loss * s;
+      }
+    }
+    store_rows4(a.out_rows, i, n, rows);
+    store_rows4(a.out_kl, i, n, kl);
+    store_rows4(a.out_weight, i, n, weight);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_down_sync(0xffffffffu, acc, o);
   if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = acc;
@@ -247,15 +320,22 @@ __global__ void __launch_bounds__(POLICY_THREADS) flce_policy_rows_kernel(const 
   if (threadIdx.x == 0) {
     double t = 0.0;
     for (int k = 0; k < POLICY_THREADS / 32; ++k) t += w[k];
-    a.blk_sum[blockIdx.x] = t;
-    __threadfence();
-    is_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    if constexpr (ONE) {
+      *a.loss = a.reduction == RED_MEAN ? t * inv_n : t;
+      *a.status = 0;
+    } else {
+      a.blk_sum[blockIdx.x] = t;
+      __threadfence();
+      is_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    }
   }
-  __syncthreads();
-  if (!is_last) return;
-  __threadfence();
-  const double t = ordered_sum<POLICY_THREADS>(a.blk_sum, gridDim.x, w);
-  if (threadIdx.x == 0) *a.loss = a.reduction == RED_MEAN ? t * inv_n : t;
+  if constexpr (!ONE) {
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    const double t = ordered_sum<POLICY_THREADS>(a.blk_sum, gridDim.x, w);
+    if (threadIdx.x == 0) *a.loss = a.reduction == RED_MEAN ? t * inv_n : t;
+  }
 }
 
 // --------------------------------------------------- losses on the logits --
@@ -275,7 +355,7 @@ struct LogitArgs {
   const int32_t* y;
   int N, V, ignore_index, reduction;
   const float* row_scale;
-  const int* n_valid;
+  RowCounts valid;
   unsigned int* ticket;
   double* row_acc;        // [N]
   float* loss;
@@ -440,7 +520,7 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
   if (tid == 0) abort_flag = 0;
   fence_mbar_init();
   __syncthreads();
-  const int n_valid = *a.n_valid;
+  const int n_valid = count_rows(a.valid);
   const double inv_n = n_valid > 0 ? 1.0 / static_cast<double>(n_valid) : 0.0;
   const int walks = a.g ? 2 : 1;
   auto next_counting = [&](int r) {

@@ -15,11 +15,13 @@ not make ``stream`` wait for the streams that produced its inputs.
 from __future__ import annotations
 
 import torch
+from torch._C import _cuda_getCurrentRawStream as _current_stream_handle  # a few us less than current_stream()
 
 from .flce import REDUCTIONS, _check, _check_tensors, alloc_workspace, load_library
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MAX_TEACHER_ENTRIES = 1024
+CLIPPED_POLICY_NO_WORKSPACE = 2048
 
 
 def _p(t):
@@ -95,21 +97,24 @@ def _run(dev, stream, inputs, allocate, call):
     allocator is told who else uses them and the inputs."""
     if stream is not None and stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-    with torch.cuda.device(dev):
-        current = torch.cuda.current_stream()
-        if stream is None or stream == current:
-            out = allocate()
-            call(out, current.cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                out = allocate()
-                call(out, stream.cuda_stream)
-            for t in out:
-                if t is not None:
-                    t.record_stream(current)
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(stream)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _run(dev, stream, inputs, allocate, call)
+    handle = _current_stream_handle(dev.index)
+    if stream is None or stream.cuda_stream == handle:
+        out = allocate()
+        call(out, handle)
+        return out
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = allocate()
+        call(out, stream.cuda_stream)
+    for t in out:
+        if t is not None:
+            t.record_stream(current)
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
     return out
 
 
@@ -140,18 +145,18 @@ def clipped_policy(row_loss, y, old_logp, advantages, *, ref_logp=None, clip_low
     _vec(advantages, torch.float32, N, dev, "advantages")
     _vec(ref_logp, torch.float32, N, dev, "ref_logp", optional=True)
     red = _scale(row_scale, reduction, N, dev, "row_scale")
-    nbytes = lib.flce_ce_workspace_size(N, 1)
+    nbytes = lib.flce_ce_workspace_size(N, 1) if N > CLIPPED_POLICY_NO_WORKSPACE else 0
 
     def allocate():
         return (torch.empty(1, dtype=torch.float64, device=dev), torch.empty(N, dtype=torch.float32, device=dev),
                 torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev),
-                torch.empty(1, dtype=torch.int32, device=dev), _workspace(workspace, nbytes, dev))
+                torch.empty(1, dtype=torch.int32, device=dev), _workspace(workspace, nbytes, dev) if nbytes else None)
 
     def call(o, s):
         loss, rows, kl, weight, status, ws = o
         _check(lib.flce_clipped_policy(_p(row_loss), _p(y), N, ignore_index, _p(old_logp), _p(advantages),
                                        _p(ref_logp), clip_low, clip_high, kl_coef, red, _p(row_scale), _p(loss),
-                                       _p(rows), _p(kl), _p(weight), _p(status), _p(ws), ws.numel(), s),
+                                       _p(rows), _p(kl), _p(weight), _p(status), _p(ws), nbytes, s),
                "flce_clipped_policy")
 
     return _run(dev, stream, (row_loss, y, old_logp, advantages, ref_logp, row_scale), allocate, call)[:5]

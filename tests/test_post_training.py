@@ -162,10 +162,10 @@ def _clipped(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(row_loss=None), 1), (dict(adv=None), 1), (dict(w=None), 1), (dict(ws=None), 1), (dict(N=0), 1),
+    (dict(row_loss=None), 1), (dict(adv=None), 1), (dict(w=None), 1), (dict(ws=None, N=5000), 1), (dict(N=0), 1),
     (dict(N=(1 << 30) + 1), 1), (dict(lo=-0.1), 1), (dict(lo=1.1), 1), (dict(hi=NAN), 1), (dict(kl=INF), 1),
     (dict(ref=None), 1), (dict(red=3), 1), (dict(loss=FAKE + 4), 2), (dict(adv=FAKE + 2), 2), (dict(ws=FAKE + 128), 2),
-    (dict(nbytes=64), 3)])
+    (dict(nbytes=64, N=5000), 3)])
 def test_clipped_policy_refusals(lib, kw, status):
     assert _clipped(lib, **kw) == status
 

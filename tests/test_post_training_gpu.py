@@ -361,7 +361,7 @@ def test_distill_id_out_of_range():
 # ----------------------------------------------------------------- policy rows --
 
 
-@pytest.mark.parametrize("N", [1, 2, 31, 256, 257, 5000, 40000])
+@pytest.mark.parametrize("N", [1, 2, 31, 256, 257, 2048, 2049, 5000, 40000])
 @pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
 def test_clipped_policy_rows(N, reduction):
     F = _lib()
