@@ -118,7 +118,7 @@ CeLayout ce_ws_layout(int64_t N) {
 // Area behind the head's workspace for a distillation call: each row's sorted
 // list of vocabulary entries and its constants.
 struct ListLayout {
-  size_t ids, c, z, count, dense, kconst, klse, kdot, total;
+  size_t list, count, dense, kconst, klse, part_dot, total;
 };
 ListLayout list_layout(int64_t N, int64_t K, size_t off) {
   ListLayout L{};
@@ -128,14 +128,12 @@ ListLayout list_layout(int64_t N, int64_t K, size_t off) {
     return o;
   };
   const size_t n = static_cast<size_t>(N), e = n * (static_cast<size_t>(K) + 1);
-  L.ids = take(e * 4);
-  L.c = take(e * 4);
-  L.z = take(e * 4);
+  L.list = take(e * 8);
   L.count = take(n * 4);
   L.dense = take(n * 4);
   L.kconst = take(n * 8);
   L.klse = take(n * 8);
-  L.kdot = take(n * 8);
+  L.part_dot = take(n * MAX_SPLITS * 8);
   L.total = off;
   return L;
 }
@@ -520,18 +518,14 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     t.ce = in.ce;
     t.perm = perm;
     t.y = y_perm;
-    t.list_ids = reinterpret_cast<int32_t*>(ws + E.ids);
-    t.list_c = reinterpret_cast<float*>(ws + E.c);
-    t.list_z = reinterpret_cast<float*>(ws + E.z);
+    t.list = reinterpret_cast<int2*>(ws + E.list);
     t.list_count = reinterpret_cast<int*>(ws + E.count);
     t.list_dense = reinterpret_cast<float*>(ws + E.dense);
     t.list_const = reinterpret_cast<double*>(ws + E.kconst);
     t.list_lse = reinterpret_cast<double*>(ws + E.klse);
-    t.list_dot = reinterpret_cast<double*>(ws + E.kdot);
     t.status = d_status;
-    a.list_ids = t.list_ids;
-    a.list_c = t.list_c;
-    a.list_z = t.list_z;
+    a.list = t.list;
+    a.part_dot = reinterpret_cast<double*>(ws + E.part_dot);
     a.list_count = t.list_count;
     a.list_dense = t.list_dense;
     a.list_stride = in.K + 1;
@@ -618,14 +612,6 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
       if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
     }
   }
-  if (opt.teacher) {
-    const int grid = static_cast<int>(std::min<int64_t>((N + 7) / 8, static_cast<int64_t>(di.num_sms) * 8));
-    size_t slot;
-    prof_begin(stream, KIND_TEACHER, &slot);
-    flce_list_dot_kernel<<<grid, 256, 0, stream>>>(t);
-    prof_end(stream, slot);
-    if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
-  }
   // Combine the splits: lse, loss, n_valid, 1/n.
   {
     CombineArgs c{};
@@ -665,7 +651,7 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     if (opt.teacher) {
       c.list_const = t.list_const;
       c.list_lse = t.list_lse;
-      c.list_dot = t.list_dot;
+      c.part_dot = a.part_dot;
     }
     const int grid = static_cast<int>((N + COMBINE_THREADS - 1) / COMBINE_THREADS);
     size_t slot;

@@ -146,9 +146,8 @@ struct GemmArgs {
   // Distillation (the kernels' LIST instantiations): each row's entries of the
   // vocabulary where G is not the softmax alone, ascending by id, and the
   // softmax taken at a temperature
-  const int32_t* list_ids;       // [N][list_stride]
-  const float* list_c;           // [N][list_stride] coefficient subtracted there (times the row's weight)
-  float* list_z;                 // [N][list_stride] the logit there (pass 1 writes it)
+  const int2* list;              // [N][list_stride] id, coefficient c (fp32 bits) subtracted there (times the row's weight)
+  double* part_dot;              // [splits][N] pass 1: sum of c z over the entries in the split
   const int* list_count;         // [N]
   const float* list_dense;       // [N] factor of the softmax in G (times the row's weight)
   int list_stride;
@@ -215,34 +214,41 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t base, int k) {
 // ------------------------------------------------------------- epilogues --
 
 // A walk along one row's list of vocabulary entries, in step with the columns
-// that an epilogue reads.
+// that an epilogue reads.  It holds two entries, so that the load of a further
+// one is not waited for unless three share 32 columns.
+constexpr int LIST_END = 0x7fffffff;  // the id behind the last entry
 struct ListWalk {
-  size_t base;    // the row's first slot
-  int pos, end;
-  int next;       // vocabulary id of the entry at pos (INT_MAX: none left)
+  const int2 *at, *end;  // the entry after `then`, the end of the row's list
+  int2 next, then;
 };
 
-// The row's first entry at or behind column col0 (binary search).
+__device__ __forceinline__ int2 list_take(ListWalk& w) {
+  const int2 e = w.at < w.end ? *w.at : make_int2(LIST_END, 0);
+  ++w.at;
+  return e;
+}
+
+// The row's first entries at or behind column col0 (binary search).
 __device__ __forceinline__ ListWalk list_begin(const GemmArgs& a, int row, bool has, int col0) {
   ListWalk w;
-  w.base = static_cast<size_t>(row) * a.list_stride;
-  w.end = has ? a.list_count[row] : 0;
-  int lo = 0, hi = w.end;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a.list_ids[w.base + mid] < col0)
-      lo = mid + 1;
+  w.at = a.list + (has ? static_cast<size_t>(row) * a.list_stride : 0);
+  w.end = w.at + (has ? a.list_count[row] : 0);
+  const int2* hi = w.end;
+  while (w.at < hi) {
+    const int2* mid = w.at + (hi - w.at) / 2;
+    if (mid->x < col0)
+      w.at = mid + 1;
     else
       hi = mid;
   }
-  w.pos = lo;
-  w.next = lo < w.end ? a.list_ids[w.base + lo] : 0x7fffffff;
+  w.next = list_take(w);
+  w.then = list_take(w);
   return w;
 }
 
-__device__ __forceinline__ void list_step(const GemmArgs& a, ListWalk& w) {
-  ++w.pos;
-  w.next = w.pos < w.end ? a.list_ids[w.base + w.pos] : 0x7fffffff;
+__device__ __forceinline__ void list_step(ListWalk& w) {
+  w.next = w.then;
+  w.then = list_take(w);
 }
 
 struct LseState {
@@ -250,6 +256,7 @@ struct LseState {
   int yr, row;
   bool has_zy;
   ListWalk list;  // LIST only
+  double dot;
 };
 
 // Pass 1: fold one [128 x 256] logit tile into the running (max, sum) of the row.
@@ -272,14 +279,15 @@ __device__ __forceinline__ void epi_lse_tile(const GemmArgs& a, uint32_t taddr, 
       st.has_zy = true;
     }
     if constexpr (LIST) {
-      while (st.list.next < col0 + 32) {
-        const int o = st.list.next - col0;
+      while (st.list.next.x < col0 + 32) {
+        const int o = st.list.next.x - col0;
         float z = 0.f;
 #pragma unroll
         for (int t = 0; t < 32; ++t)
           if (t == o) z = __uint_as_float(r[t]);
-        a.list_z[st.list.base + st.list.pos] = z;
-        list_step(a, st.list);
+        const float c = __int_as_float(st.list.next.y);
+        if (c != 0.f) st.dot += static_cast<double>(c) * static_cast<double>(z);
+        list_step(st.list);
       }
       __syncwarp();
     }
@@ -356,7 +364,8 @@ __device__ __forceinline__ void stage_and_store(EpiStage& es, int lane, const CU
 // Pass 2: G = valid * (softmax - onehot) / n for one tile, stored as bf16.
 template <bool LIST>
 __device__ __forceinline__ void epi_grad_tile(const GemmArgs& a, int vbase, uint32_t taddr, int row0, int nb,
-                                              int row_local, EpiStage& es, const CUtensorMap* mapG) {
+                                              int row_local, EpiStage& es, const CUtensorMap* mapG,
+                                              ListWalk walk) {
   const int row = row0 + row_local;
   const int lane = row_local & 31;
   const bool in_rows = row < a.N;
@@ -367,8 +376,6 @@ __device__ __forceinline__ void epi_grad_tile(const GemmArgs& a, int vbase, uint
   if (a.row_mult && valid) scale *= a.row_mult[row];
   const float zs = LIST ? a.zs : LOG2E;
   const float dense = LIST && valid ? scale * a.list_dense[row] : scale;
-  ListWalk walk;
-  if constexpr (LIST) walk = list_begin(a, row, valid, vbase + nb * BN);
   const int wrow0 = row0 + (row_local & ~31);
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
@@ -382,13 +389,13 @@ __device__ __forceinline__ void epi_grad_tile(const GemmArgs& a, int vbase, uint
       for (int t = 0; t < 32; ++t)
         g[t] = (valid && t < lim) ? ex2_approx(fmaf(__uint_as_float(r[t]), zs, -l2)) * dense : 0.f;
       if constexpr (LIST) {
-        while (walk.next < colg0 + 32) {
-          const int o = walk.next - colg0;
-          const float sub = a.list_c[walk.base + walk.pos] * scale;
+        while (walk.next.x < colg0 + 32) {
+          const int o = walk.next.x - colg0;
+          const float sub = __int_as_float(walk.next.y) * scale;
 #pragma unroll
           for (int t = 0; t < 32; ++t)
             if (t == o) g[t] -= sub;
-          list_step(a, walk);
+          list_step(walk);
         }
         __syncwarp();
       } else {
@@ -855,7 +862,10 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
       st.run_l = 0.f;
       st.zy_val = 0.f;
       st.has_zy = false;
-      if constexpr (LIST) st.list = list_begin(a, st.row, st.row < a.N, nb0 * BN);
+      if constexpr (LIST) {
+        st.list = list_begin(a, st.row, st.row < a.N, nb0 * BN);
+        st.dot = 0.0;
+      }
       for (int nb = nb0; nb < nb1; ++nb) {
         // a pair of tiles (nb, nb + 1) sits in buffers acc and acc ^ 1, and the
         // tile after it in acc again (the issuer's sequence)
@@ -880,6 +890,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
         a.part_m[static_cast<size_t>(split + a.split_off) * a.N + st.row] = st.run_m;
         a.part_l[static_cast<size_t>(split + a.split_off) * a.N + st.row] = st.run_l;
         if (st.has_zy) a.zy[st.row] = st.zy_val;
+        if constexpr (LIST) a.part_dot[static_cast<size_t>(split) * a.N + st.row] = st.dot;
       }
     }
   }
@@ -1383,6 +1394,11 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
       const Item it = decode_item(a, u);
       const int vbase = it.c * a.Vc;
       const int row0 = it.a * CM + rank * BM;
+      ListWalk walk{};
+      if constexpr (LIST) {  // found while the tile is still being computed
+        const int row = row0 + row_local;
+        if (it.kind == ITEM_GRAD) walk = list_begin(a, row, row < a.N, vbase + it.b * BN);
+      }
       // wait for the previous readers (G) / writers (dX) of what this tile writes
       if (lane == 0) {
         if (it.kind == ITEM_GRAD && it.c > 0) {
@@ -1443,7 +1459,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
         // zero, written once by the first chunk
         if (it.kind == ITEM_DX && it.c == 0) epi_zero_tile(taddr, row0, it.b, row_local, es, &m.Hio);
       } else if (it.kind == ITEM_GRAD) {
-        epi_grad_tile<LIST>(a, vbase, taddr, row0, it.b, row_local, es, &m.Go);
+        epi_grad_tile<LIST>(a, vbase, taddr, row0, it.b, row_local, es, &m.Go, walk);
       } else if (it.kind == ITEM_DW) {
         const int nt = dw_first_tile(a, it);
         if (any_valid)
@@ -1643,10 +1659,10 @@ struct CombineArgs {
   PolicyArgs pol;
   float* logp;      // [N]
   float* row_mult;  // [N] d L_i / d l_i; may be zy itself
-  // Distillation: the row's loss is list_const + list_lse lse - list_dot (all null otherwise)
+  // Distillation: the row's loss is list_const + list_lse lse - the sum of part_dot (all null otherwise)
   const double* list_const;
   const double* list_lse;
-  const double* list_dot;
+  const double* part_dot;  // [splits][N]
   const int* perm;  // row of the caller behind each row of y, part_m, ... (token-row order)
   const int* mean_count;  // optional: divide the mean by this count instead of n_valid
   const int32_t* y;
@@ -1694,8 +1710,10 @@ __global__ void __launch_bounds__(COMBINE_THREADS) flce_combine_kernel(const Com
       l2 = (M + logf(S)) * LOG2E;
     } else {
       float M = -INFINITY;
+#pragma unroll 8
       for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.part_m[static_cast<size_t>(s) * a.N + i]);
       float L = 0.f;
+#pragma unroll 8
       for (int s = 0; s < a.splits; ++s)
         L += a.part_l[static_cast<size_t>(s) * a.N + i] * exp2f(a.part_m[static_cast<size_t>(s) * a.N + i] - M);
       l2 = M + log2f(L);
@@ -1711,7 +1729,12 @@ __global__ void __launch_bounds__(COMBINE_THREADS) flce_combine_kernel(const Com
     double row = 0.0;
     if (valid) {
       row = static_cast<double>(l2) * LN2 - static_cast<double>(zyi);
-      if (a.list_dot) row = a.list_const[i] + a.list_lse[i] * (static_cast<double>(l2) * LN2) - a.list_dot[i];
+      if (a.part_dot) {
+        double dot = 0.0;
+#pragma unroll 8
+        for (int s = 0; s < a.splits; ++s) dot += a.part_dot[static_cast<size_t>(s) * a.N + i];
+        row = a.list_const[i] + a.list_lse[i] * (static_cast<double>(l2) * LN2) - dot;
+      }
       vi = 1;
       // mean and sum add the plain row losses (the mean divides at the end)
       li = a.reduction == RED_NONE && a.grad_row_scale ? row * static_cast<double>(a.grad_row_scale[i]) : row;

@@ -957,14 +957,11 @@ struct TeacherArgs {
   const int* perm;        // row of the caller behind each row
   const int32_t* y;       // targets in the rows' order
   // outputs, in the rows' order
-  int32_t* list_ids;      // [N][K + 1]
-  float* list_c;
-  float* list_z;          // read by flce_list_dot_kernel
+  int2* list;             // [N][K + 1]
   int* list_count;
   float* list_dense;
   double* list_const;
   double* list_lse;
-  double* list_dot;
   int* status;
 };
 
@@ -1045,27 +1042,9 @@ __global__ void __launch_bounds__(TEACHER_THREADS) flce_teacher_lists_kernel(con
       for (int j = 0; j < K1; ++j) rank += s_id[j] < id || (s_id[j] == id && j < k) ? 1 : 0;
       double c = a.ce;
       if (k < a.K) c = ts.any ? static_cast<double>(expf(static_cast<float>(static_cast<double>(s_u[k]) * a.inv_T - ts.shift))) * a.kd * a.inv_T : 0.0;
-      a.list_ids[out + rank] = id;
-      a.list_c[out + rank] = static_cast<float>(c);
+      a.list[out + rank] = make_int2(id, __float_as_int(static_cast<float>(c)));
     }
     __syncthreads();
-  }
-}
-
-// sum_k c_k z_k of each row, in fp64 (one warp per row, fixed order).
-__global__ void __launch_bounds__(256) flce_list_dot_kernel(const TeacherArgs a) {
-  const int lane = threadIdx.x & 31;
-  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < a.N; i += gridDim.x * 8) {
-    const size_t at = static_cast<size_t>(i) * (a.K + 1);
-    const int n = a.list_count[i];
-    double s = 0.0;
-    for (int k = lane; k < n; k += 32) {
-      const float c = a.list_c[at + k];
-      if (!(c == 0.f)) s += static_cast<double>(c) * static_cast<double>(a.list_z[at + k]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) a.list_dot[i] = s;
   }
 }
 
