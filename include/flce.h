@@ -396,7 +396,12 @@ flce_status_t flce_distill_topk(const void* logits, int32_t dtype, int64_t ld, c
  * cross-entropy call, where separate calls (row losses, flce_clipped_policy,
  * gradients) run pass 1 twice.  d_logp (fp32 [N]) receives lp_i, 0 on ignored
  * rows.  Other arguments and results as flce_forward_backward_ex (dX and dW
- * both NULL: loss and log-probabilities only) and flce_clipped_policy. */
+ * both NULL: loss and log-probabilities only) and flce_clipped_policy.
+ * workspace: flce_policy_workspace_size bytes (`reorder` != 0: with the area
+ * that lets the call reorder token rows), which depends on V: small batches
+ * take wider vocabulary chunks.  flce_workspace_size bytes are enough, at the
+ * cross-entropy head's chunk width.  0 for invalid sizes. */
+size_t flce_policy_workspace_size(int64_t N, int64_t H, int64_t V, int32_t reorder);
 flce_status_t flce_policy_forward_backward(const uint16_t* X, const uint16_t* W, const int32_t* y, int64_t N,
                                            int64_t H, int64_t V, int32_t ignore_index, const float* d_old_logp,
                                            const float* d_advantage, const float* d_ref_logp, double clip_low,
@@ -409,10 +414,10 @@ flce_status_t flce_policy_forward_backward(const uint16_t* X, const uint16_t* W,
  * arguments as flce_distill_topk, except that ce_weight needs temperature 1
  * (FLCE_ERR_UNSUPPORTED otherwise: a logit tile is turned into one softmax);
  * other arguments as flce_forward_backward_ex.  workspace:
- * flce_distill_workspace_size(N, H, K, 0) bytes, or with `reorder` != 0 the
- * size that lets the call reorder token rows; both independent of V, 0 for
- * invalid sizes. */
-size_t flce_distill_workspace_size(int64_t N, int64_t H, int32_t K, int32_t reorder);
+ * flce_distill_workspace_size bytes, as flce_policy_workspace_size with the
+ * rows' entry lists behind it (the same query with V = 1 gives the least that a
+ * call takes). */
+size_t flce_distill_workspace_size(int64_t N, int64_t H, int64_t V, int32_t K, int32_t reorder);
 flce_status_t flce_distill_forward_backward(const uint16_t* X, const uint16_t* W, const int32_t* y, int64_t N,
                                             int64_t H, int64_t V, int32_t ignore_index, const int32_t* d_teacher_ids,
                                             const void* d_teacher_logits, int32_t teacher_dtype, int32_t K,

@@ -35,4 +35,5 @@ from .post_training import (  # noqa: F401
     distill_workspace_size,
     policy_forward_backward,
     policy_loss,
+    policy_workspace_size,
 )

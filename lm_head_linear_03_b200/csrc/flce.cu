@@ -22,6 +22,21 @@ using namespace flce;
 // Vocabulary entries per pass-2 chunk.  The G chunk buffer is N x VC bf16, so
 // the workspace stays independent of V.
 constexpr int VC = 2048;
+// The post-training heads, whose workspace may depend on V, take wider chunks
+// while G stays within 64 MB (half the L2): a chunk's first items wait for the
+// last ones of the chunk before, which is most of a small head's time, and the
+// running dX sum is read and written once per chunk.  Measured against 2048
+// (N x H x V): 256 x 256 x 4096 62 against 76 us, 16 x 4096 x 128256 1.45
+// against 3.17 ms, 512 x 4096 x 128256 2.07 against 3.30 ms, 2048 x 2304 x
+// 256000 6.7 against 7.5 ms.  G of 16 MB is 2 to 7% slower from 1024 rows on,
+// 128 MB the same as 64.
+constexpr int64_t WIDE_G_BYTES = 64ll << 20;
+constexpr int64_t WIDE_CHUNK = 65536;
+int wide_chunk(int64_t N, int64_t V) {
+  const int64_t most = std::max<int64_t>(VC, std::min(WIDE_CHUNK, WIDE_G_BYTES / (2 * N)) / BN * BN);
+  const int64_t chunks = (V + most - 1) / most;
+  return static_cast<int>(std::max<int64_t>(VC, ((V + chunks - 1) / chunks + BN - 1) / BN * BN));
+}
 // Active k-blocks a paired dW item runs on its first half before it needs the
 // second buffer: about one dX epilogue's time on the previous item.
 constexpr int DW_LEAD = 16;
@@ -45,6 +60,7 @@ struct WsLayout {
   size_t ctrl, counters, counters_bytes, tile_cnt, tile_valid, perm, y_perm, g_perm, lse2, zy, part_m, part_l,
       blk_loss, blk_cnt, G, lo, xc, total;
   bool packed;  // holds xc, the packed copy of X that reordered rows need
+  int chunk;    // vocabulary entries per pass-2 chunk
 };
 
 // ctrl block: [0] status, [4] ticket, [8] n_valid, [12] inv_n, [16] loss,
@@ -60,8 +76,9 @@ struct Ctrl {
 };
 
 // `packed`: with the N x H area for the packed copy of X (reordered rows).
-WsLayout ws_layout(int64_t N, int64_t H, bool packed = false) {
+WsLayout ws_layout(int64_t N, int64_t H, bool packed = false, int chunk = VC) {
   WsLayout L{};
+  L.chunk = chunk;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -71,9 +88,9 @@ WsLayout ws_layout(int64_t N, int64_t H, bool packed = false) {
   const size_t n = static_cast<size_t>(N);
   const size_t nblk = (n + COMBINE_THREADS - 1) / COMBINE_THREADS;
   L.ctrl = take(256);
-  // pass-2 completion counters: g_row[TM], x_row[TM], g_col[VC/BN], w_col[VC/BN]
+  // pass-2 completion counters: g_row[TM], x_row[TM], g_col[chunk/BN], w_col[chunk/BN]
   const size_t tm = (n + CM - 1) / CM;
-  L.counters_bytes = (2 * tm + 2 * (VC / BN)) * 4;
+  L.counters_bytes = (2 * tm + 2 * static_cast<size_t>(chunk / BN)) * 4;
   L.counters = take(L.counters_bytes);
   L.tile_cnt = take(tm * 4);
   L.tile_valid = take(tm * 4);
@@ -86,7 +103,7 @@ WsLayout ws_layout(int64_t N, int64_t H, bool packed = false) {
   L.part_l = take(static_cast<size_t>(MAX_SPLITS) * n * 4);
   L.blk_loss = take(nblk * 8);
   L.blk_cnt = take(nblk * 4);
-  L.G = take(n * VC * 2);
+  L.G = take(n * static_cast<size_t>(chunk) * 2);
   L.lo = take(n * static_cast<size_t>(H) * 2);
   L.packed = packed;
   L.xc = packed ? take(n * static_cast<size_t>(H) * 2) : 0;
@@ -283,7 +300,7 @@ int choose_splits(int tiles_m, int vtiles, int sms) {
   return best;
 }
 
-Plan make_plan(int64_t N, int64_t H, int64_t V, int clusters) {
+Plan make_plan(int64_t N, int64_t H, int64_t V, int clusters, int chunk = VC) {
   (void)H;
   Plan p{};
   p.clusters = clusters;
@@ -292,7 +309,7 @@ Plan make_plan(int64_t N, int64_t H, int64_t V, int clusters) {
   p.splits = choose_splits(p.tiles_m, p.vtiles, clusters);
   p.lse_clusters =
       static_cast<int>(std::min<long long>(static_cast<long long>(p.tiles_m) * p.splits, clusters));
-  p.num_chunks = static_cast<int>((V + VC - 1) / VC);
+  p.num_chunks = static_cast<int>((V + chunk - 1) / chunk);
   // prep, row order, pass 1, combine, pass 2, dX scatter (plus the X row
   // packing on a workspace with the packed-X area)
   p.launches = 6;
@@ -439,9 +456,16 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
   // reordered rows need the packed-X area: only a large enough workspace has it
   // (vocabulary shards keep the caller's order: their statistics are per row)
   const size_t list_bytes = opt.teacher ? list_layout(N, opt.teacher->K, 0).total : 0;
-  const WsLayout L =
-      ws_layout(N, H, opt.combine == COMBINE_FULL && ws_bytes >= ws_layout(N, H, true).total + list_bytes);
-  const Plan P = make_plan(N, H, V, di.max_clusters);
+  // the wide chunks first where there is a choice between them and the reordering
+  auto fits = [&](bool packed, int chunk) { return ws_bytes >= ws_layout(N, H, packed, chunk).total + list_bytes; };
+  const int wide = opt.policy || opt.teacher ? wide_chunk(N, V) : VC;
+  const bool may_pack = opt.combine == COMBINE_FULL;
+  const WsLayout L = may_pack && fits(true, wide)  ? ws_layout(N, H, true, wide)
+                     : fits(false, wide)           ? ws_layout(N, H, false, wide)
+                     : may_pack && fits(true, VC)  ? ws_layout(N, H, true)
+                                                   : ws_layout(N, H);
+  const uint64_t vc = static_cast<uint64_t>(L.chunk);
+  const Plan P = make_plan(N, H, V, di.max_clusters, L.chunk);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(ws + L.ctrl);
   float* lse2 = reinterpret_cast<float*>(ws + L.lse2);
@@ -459,13 +483,13 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
   CUtensorMap mX_k, mW_k, mG_mn, mX_mn, mG_k, mW_mn, mXc_k, mXc_mn;
   const uint64_t n = static_cast<uint64_t>(N), h = static_cast<uint64_t>(H), v = static_cast<uint64_t>(V);
   bool ok = make_map(&mX_k, X, h, n, h * 2, BK, BM) && make_map(&mW_k, W, h, v, h * 2, BK, BNH) &&
-            make_map(&mG_mn, G, VC, n, VC * 2, 64, BK) && make_map(&mX_mn, X, h, n, h * 2, 64, BK) &&
-            make_map(&mG_k, G, VC, n, VC * 2, BK, BM) && make_map(&mW_mn, W, h, v, h * 2, 64, BK) &&
+            make_map(&mG_mn, G, vc, n, vc * 2, 64, BK) && make_map(&mX_mn, X, h, n, h * 2, 64, BK) &&
+            make_map(&mG_k, G, vc, n, vc * 2, BK, BM) && make_map(&mW_mn, W, h, v, h * 2, 64, BK) &&
             // the packed copy of X (the caller's X stands in when there is none: never read then)
             make_map(&mXc_k, Xc ? Xc : X, h, n, h * 2, BK, BM) && make_map(&mXc_mn, Xc ? Xc : X, h, n, h * 2, 64, BK);
   // 32 x 32 output boxes of the epilogues (64-byte swizzle)
   CUtensorMap mGo, mDWo, mHio, mLoo;
-  ok = ok && (dX == nullptr || (make_map(&mGo, G, VC, n, VC * 2, EPI_BOX, EPI_BOX, Swz::k64) &&
+  ok = ok && (dX == nullptr || (make_map(&mGo, G, vc, n, vc * 2, EPI_BOX, EPI_BOX, Swz::k64) &&
                                 make_map(&mDWo, dW, h, v, h * 2, EPI_BOX, EPI_BOX, Swz::k64) &&
                                 make_map(&mHio, dX, h, n, h * 2, EPI_BOX, EPI_BOX, Swz::k64) &&
                                 make_map(&mLoo, lo, h, n, h * 2, EPI_BOX, EPI_BOX, Swz::k64)));
@@ -481,7 +505,7 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
   a.H = static_cast<int>(H);
   a.V = static_cast<int>(V);
   a.ignore_index = ignore_index;
-  a.Vc = VC;
+  a.Vc = L.chunk;
   a.y = y_perm;
   a.part_m = part_m;
   a.part_l = part_l;
@@ -668,8 +692,8 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     b.HN = static_cast<int>((H + BN - 1) / BN);
     b.dw_lead = DW_LEAD;
     b.C = P.num_chunks;
-    b.VTf = VC / BN;
-    b.VT_last = static_cast<int>((V - static_cast<int64_t>(P.num_chunks - 1) * VC + BN - 1) / BN);
+    b.VTf = L.chunk / BN;
+    b.VT_last = static_cast<int>((V - static_cast<int64_t>(P.num_chunks - 1) * L.chunk + BN - 1) / BN);
     if (b.C == 1) b.VTf = b.VT_last;
     // G tiles column by column when a chunk holds more than three rounds of
     // them for the SM pairs, else row by row (see the queue's description)
@@ -692,7 +716,7 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     b.g_row = ctr;
     b.x_row = ctr + b.TM;
     b.g_col = ctr + 2 * b.TM;
-    b.w_col = ctr + 2 * b.TM + VC / BN;
+    b.w_col = ctr + 2 * b.TM + L.chunk / BN;
     Pass2Maps pm;
     pm.Xk = mX_k;
     pm.Wk = mW_k;
@@ -730,7 +754,8 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
       }
       if (opt.pipe) {  // dW rows of chunks c0 .. c1-1 are final
         const PipeCtx& pp = *opt.pipe;
-        const int64_t r0 = static_cast<int64_t>(c0) * VC, r1 = std::min<int64_t>(V, static_cast<int64_t>(c1) * VC);
+        const int64_t r0 = static_cast<int64_t>(c0) * L.chunk;
+        const int64_t r1 = std::min<int64_t>(V, static_cast<int64_t>(c1) * L.chunk);
         if (pp.section_rows) {
           pp.section_rows[k] = r0;
           pp.section_rows[k + 1] = r1;
@@ -1321,9 +1346,14 @@ flce_status_t flce_policy_forward_backward(const uint16_t* X, const uint16_t* W,
   return enqueue(X, W, y, N, H, V, ignore_index, d_loss, d_status, dX, dW, workspace, workspace_bytes, stream, opt);
 }
 
-size_t flce_distill_workspace_size(int64_t N, int64_t H, int32_t K, int32_t reorder) {
-  if (check_sizes(N, H, 1) != FLCE_OK || K <= 0 || K > DISTILL_MAX_K) return 0;
-  return list_layout(N, K, ws_layout(N, H, reorder != 0).total).total;
+size_t flce_policy_workspace_size(int64_t N, int64_t H, int64_t V, int32_t reorder) {
+  if (check_sizes(N, H, V) != FLCE_OK) return 0;
+  return ws_layout(N, H, reorder != 0, wide_chunk(N, V)).total;
+}
+
+size_t flce_distill_workspace_size(int64_t N, int64_t H, int64_t V, int32_t K, int32_t reorder) {
+  if (check_sizes(N, H, V) != FLCE_OK || K <= 0 || K > DISTILL_MAX_K) return 0;
+  return ws_layout(N, H, reorder != 0, wide_chunk(N, V)).total + list_layout(N, K, 0).total;
 }
 
 flce_status_t flce_distill_forward_backward(const uint16_t* X, const uint16_t* W, const int32_t* y, int64_t N,
@@ -1345,7 +1375,7 @@ flce_status_t flce_distill_forward_backward(const uint16_t* X, const uint16_t* W
   if (!aligned(grad_row_scale, 4) || !aligned(d_mean_count, 4) || !aligned(d_loss, 4) || !aligned(d_row_loss, 4) ||
       !aligned(d_status, 4))
     return FLCE_ERR_UNSUPPORTED;
-  if (workspace_bytes < flce_distill_workspace_size(N, H, K, 0)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < ws_layout(N, H).total + list_layout(N, K, 0).total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   TeacherIn t{};
   t.ids = d_teacher_ids;
   t.logits = d_teacher_logits;

@@ -56,6 +56,7 @@ EXPORTED = (
     "flce_policy_loss",
     "flce_distill_topk",
     "flce_policy_forward_backward",
+    "flce_policy_workspace_size",
     "flce_distill_workspace_size",
     "flce_distill_forward_backward",
 )
@@ -167,7 +168,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.flce_policy_forward_backward.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, vp, vp, dbl, dbl, dbl, i32, vp, vp,
                                                  vp, vp, vp, vp, vp, vp, sz, vp]
     lib.flce_policy_forward_backward.restype = ctypes.c_int
-    lib.flce_distill_workspace_size.argtypes = [i64, i64, i32, i32]
+    lib.flce_policy_workspace_size.argtypes = [i64, i64, i64, i32]
+    lib.flce_policy_workspace_size.restype = sz
+    lib.flce_distill_workspace_size.argtypes = [i64, i64, i64, i32, i32]
     lib.flce_distill_workspace_size.restype = sz
     lib.flce_distill_forward_backward.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, vp, i32, i32, vp, dbl, dbl, dbl,
                                                   i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]

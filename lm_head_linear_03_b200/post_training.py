@@ -17,7 +17,7 @@ from __future__ import annotations
 import torch
 from torch._C import _cuda_getCurrentRawStream as _current_stream_handle  # a few us less than current_stream()
 
-from .flce import REDUCTIONS, _check, _check_tensors, alloc_workspace, load_library
+from .flce import REDUCTIONS, _check, _check_tensors, load_library
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MAX_TEACHER_ENTRIES = 1024
@@ -235,6 +235,13 @@ def _head_outputs(X, W, grads):
     return (torch.empty_like(X), torch.empty_like(W)) if grads else (None, None)
 
 
+def policy_workspace_size(N: int, H: int, V: int, reorder: bool = False) -> int:
+    """flce_policy_workspace_size: bytes one :func:`policy_forward_backward` takes,
+    or with ``reorder`` those that let it skip scattered ignored rows.  It also
+    runs on flce_workspace_size bytes, small batches more slowly."""
+    return int(load_library().flce_policy_workspace_size(N, H, V, 1 if reorder else 0))
+
+
 def policy_forward_backward(X, W, y, old_logp, advantages, *, ref_logp=None, clip_low: float = 0.2,
                             clip_high: float = 0.2, kl_coef: float = 0.0, reduction: str = "mean",
                             grad_row_scale=None, mean_count=None, ignore_index: int = -100, grads: bool = True,
@@ -256,7 +263,8 @@ def policy_forward_backward(X, W, y, old_logp, advantages, *, ref_logp=None, cli
     def allocate():
         return (torch.empty(1, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev),
                 torch.empty(N, dtype=torch.float32, device=dev), *_head_outputs(X, W, grads),
-                alloc_workspace(N, H, V, dev) if workspace is None else workspace)
+                torch.empty(policy_workspace_size(N, H, V), dtype=torch.uint8, device=dev)
+                if workspace is None else workspace)
 
     def call(o, s):
         loss, status, logp, dX, dW, ws = o
@@ -269,10 +277,10 @@ def policy_forward_backward(X, W, y, old_logp, advantages, *, ref_logp=None, cli
     return _run(dev, stream, (X, W, y, old_logp, advantages, ref_logp, grad_row_scale, mean_count), allocate, call)[:5]
 
 
-def distill_workspace_size(N: int, H: int, K: int, reorder: bool = False) -> int:
-    """flce_distill_workspace_size: bytes one :func:`distill_forward_backward`
-    needs, or with ``reorder`` those that let it skip scattered ignored rows."""
-    return int(load_library().flce_distill_workspace_size(N, H, K, 1 if reorder else 0))
+def distill_workspace_size(N: int, H: int, V: int, K: int, reorder: bool = False) -> int:
+    """flce_distill_workspace_size: as :func:`policy_workspace_size`, for
+    :func:`distill_forward_backward` with K teacher entries per row."""
+    return int(load_library().flce_distill_workspace_size(N, H, V, K, 1 if reorder else 0))
 
 
 def distill_forward_backward(X, W, y, teacher_ids, teacher_logits, *, teacher_lse=None, temperature: float = 1.0,
@@ -295,7 +303,7 @@ def distill_forward_backward(X, W, y, teacher_ids, teacher_logits, *, teacher_ls
     def allocate():
         return (torch.empty(1, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev),
                 torch.empty(N, dtype=torch.float32, device=dev) if row_loss else None, *_head_outputs(X, W, grads),
-                torch.empty(distill_workspace_size(N, H, K), dtype=torch.uint8, device=dev)
+                torch.empty(distill_workspace_size(N, H, V, K), dtype=torch.uint8, device=dev)
                 if workspace is None else workspace)
 
     def call(o, s):

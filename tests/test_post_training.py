@@ -230,13 +230,22 @@ def test_policy_head_refusals(lib, kw, status):
     assert _head_policy(lib, **kw) == status
 
 
-def test_distill_workspace_size(lib):
+def test_workspace_sizes(lib):
     from lm_head_linear_03_b200 import flce
     import lm_head_linear_03_b200 as F
-    assert F.distill_workspace_size(300, 264, 16) > flce.workspace_size(300, 264)
-    assert F.distill_workspace_size(300, 264, 16, True) - F.distill_workspace_size(300, 264, 16) == flce.packed_x_bytes(300, 264)
-    for bad in ((0, 264, 16), (300, 260, 16), (300, 264, 0), (300, 264, 1025)):
-        assert F.distill_workspace_size(*bad) == 0
+    area = flce.packed_x_bytes(300, 264)
+    for V in (1, 2048, 5003, 128256):
+        assert F.policy_workspace_size(300, 264, V) >= flce.workspace_size(300, 264)
+        assert F.distill_workspace_size(300, 264, V, 16) > F.policy_workspace_size(300, 264, V)
+        assert F.policy_workspace_size(300, 264, V, True) - F.policy_workspace_size(300, 264, V) == area
+        assert F.distill_workspace_size(300, 264, V, 16, True) - F.distill_workspace_size(300, 264, V, 16) == area
+    # the chunk buffer stays within 64 MB where it is wider than the cross-entropy head's
+    for N in (1, 300, 2048, 8192, 32768):
+        assert F.policy_workspace_size(N, 256, 256000) <= flce.workspace_size(N, 256) + (64 << 20)
+    for bad in ((0, 264, 10), (300, 260, 10), (300, 264, 0)):
+        assert F.policy_workspace_size(*bad) == 0 and F.distill_workspace_size(*bad, 4) == 0
+    for K in (0, 1025):
+        assert F.distill_workspace_size(300, 264, 10, K) == 0
 
 
 def test_binding_refuses_before_any_call(lib):

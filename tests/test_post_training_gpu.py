@@ -477,7 +477,7 @@ def test_heads_with_reordered_rows(reduction):
     _close(_np(lp), rlp, 1e-4, "logp")
     assert_grad_close(_np(dX), G @ _np(W), "dX")
     assert_grad_close(_np(dW), G.T @ _np(X), "dW")
-    ws = torch.empty(F.distill_workspace_size(N, H, K, True), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(F.distill_workspace_size(N, H, V, K, True), dtype=torch.uint8, device="cuda")
     loss, status, rows, dX, dW = F.distill_forward_backward(*d, *_cuda(ids, u), ce_weight=0.5, workspace=ws, row_loss=True,
                                                             reduction=reduction, grad_row_scale=scale)
     assert F.row_order_info(ws)[0] and status.item() == 0
