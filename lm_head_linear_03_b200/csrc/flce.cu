@@ -56,11 +56,23 @@ flce_status_t cuda_fail(int line) {
   return FLCE_ERR_CUDA;
 }
 
+// Ranges that the vocabulary of a chunk is split into for dX when the token and
+// hidden tiles alone are fewer than the SM pairs: as many items as two for each
+// pair of the 74 a B200 has, of 16 k-blocks at least.
+int dx_splits(int64_t N, int64_t H, int64_t V, int chunk) {
+  const int64_t tiles = ((N + CM - 1) / CM) * ((H + BN - 1) / BN);
+  if (tiles >= 74) return 1;
+  const int64_t last = V % chunk ? V % chunk : chunk;  // no range of any chunk may be empty
+  const int64_t most = std::min<int64_t>((last + BK - 1) / BK, std::max<int64_t>(1, std::min<int64_t>(V, chunk) / (16 * BK)));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(148 + tiles - 1) / tiles, most, 64})));
+}
+
 struct WsLayout {
   size_t ctrl, counters, counters_bytes, tile_cnt, tile_valid, perm, y_perm, g_perm, lse2, zy, part_m, part_l,
-      blk_loss, blk_cnt, G, lo, xc, total;
+      blk_loss, blk_cnt, G, lo, xc, part, total;
   bool packed;  // holds xc, the packed copy of X that reordered rows need
   int chunk;    // vocabulary entries per pass-2 chunk
+  int splits;   // vocabulary ranges of dX, with fp32 sums in `part`
 };
 
 // ctrl block: [0] status, [4] ticket, [8] n_valid, [12] inv_n, [16] loss,
@@ -76,9 +88,10 @@ struct Ctrl {
 };
 
 // `packed`: with the N x H area for the packed copy of X (reordered rows).
-WsLayout ws_layout(int64_t N, int64_t H, bool packed = false, int chunk = VC) {
+WsLayout ws_layout(int64_t N, int64_t H, bool packed = false, int chunk = VC, int splits = 1) {
   WsLayout L{};
   L.chunk = chunk;
+  L.splits = splits;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -107,8 +120,15 @@ WsLayout ws_layout(int64_t N, int64_t H, bool packed = false, int chunk = VC) {
   L.lo = take(n * static_cast<size_t>(H) * 2);
   L.packed = packed;
   L.xc = packed ? take(n * static_cast<size_t>(H) * 2) : 0;
+  L.part = splits > 1 ? take(n * static_cast<size_t>(H) * 4 * splits) : 0;
   L.total = off;
   return L;
+}
+
+// A post-training head's own layout.
+WsLayout wide_layout(int64_t N, int64_t H, int64_t V, bool packed) {
+  const int chunk = wide_chunk(N, V);
+  return ws_layout(N, H, packed, chunk, dx_splits(N, H, V, chunk));
 }
 
 // Workspace of the cross-entropy-on-logits entry: depends on N only.
@@ -456,14 +476,13 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
   // reordered rows need the packed-X area: only a large enough workspace has it
   // (vocabulary shards keep the caller's order: their statistics are per row)
   const size_t list_bytes = opt.teacher ? list_layout(N, opt.teacher->K, 0).total : 0;
-  // the wide chunks first where there is a choice between them and the reordering
-  auto fits = [&](bool packed, int chunk) { return ws_bytes >= ws_layout(N, H, packed, chunk).total + list_bytes; };
-  const int wide = opt.policy || opt.teacher ? wide_chunk(N, V) : VC;
-  const bool may_pack = opt.combine == COMBINE_FULL;
-  const WsLayout L = may_pack && fits(true, wide)  ? ws_layout(N, H, true, wide)
-                     : fits(false, wide)           ? ws_layout(N, H, false, wide)
-                     : may_pack && fits(true, VC)  ? ws_layout(N, H, true)
-                                                   : ws_layout(N, H);
+  // the heads' own layout first where there is a choice between it and the reordering
+  auto fits = [&](const WsLayout& l) { return ws_bytes >= l.total + list_bytes; };
+  const bool own = opt.policy || opt.teacher, may_pack = opt.combine == COMBINE_FULL;
+  const WsLayout L = own && fits(wide_layout(N, H, V, true))    ? wide_layout(N, H, V, true)
+                     : own && fits(wide_layout(N, H, V, false)) ? wide_layout(N, H, V, false)
+                     : may_pack && fits(ws_layout(N, H, true))  ? ws_layout(N, H, true)
+                                                                : ws_layout(N, H);
   const uint64_t vc = static_cast<uint64_t>(L.chunk);
   const Plan P = make_plan(N, H, V, di.max_clusters, L.chunk);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -690,6 +709,8 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     GemmArgs b = a;
     b.TM = P.tiles_m;
     b.HN = static_cast<int>((H + BN - 1) / BN);
+    b.KS = L.splits;
+    b.dx_part = L.splits > 1 ? reinterpret_cast<float*>(ws + L.part) : nullptr;
     b.dw_lead = DW_LEAD;
     b.C = P.num_chunks;
     b.VTf = L.chunk / BN;
@@ -707,7 +728,7 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     long long total = static_cast<long long>(b.C == 1 ? b.VT_last : b.VTf) * b.TM;  // G(0)
     for (int c = 0; c < b.C; ++c) {
       const long long vt = c == b.C - 1 ? b.VT_last : b.VTf;
-      total += static_cast<long long>(b.TM) * b.HN + vt * b.HW;
+      total += static_cast<long long>(b.TM) * b.HN * b.KS + vt * b.HW;
       if (c + 1 < b.C) total += static_cast<long long>(c + 1 == b.C - 1 ? b.VT_last : b.VTf) * b.TM;
       section_end[c] = total;
     }
@@ -771,11 +792,17 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
         }
       }
     }
-    // reordered rows: the final dX rows go back in place (no-op otherwise)
-    const int sgrid = static_cast<int>(std::min<int64_t>((N + 7) / 8, static_cast<int64_t>(di.num_sms) * 8));
     prof_begin(stream, KIND_SCATTER, &slot);
-    flce_dx_scatter_kernel<<<sgrid, 256, 0, stream>>>(lo, dX, perm, &ctrl->reordered, &ctrl->n_rows,
-                                                      static_cast<int>(N), static_cast<int>(H));
+    if (L.splits > 1) {
+      const int64_t blocks = (N * (H / 8) + 255) / 256;
+      flce_dx_join_kernel<<<static_cast<int>(std::min<int64_t>(blocks, static_cast<int64_t>(di.num_sms) * 8)), 256, 0,
+                            stream>>>(b.dx_part, L.splits, dX, perm, a.tile_valid, static_cast<int>(N),
+                                      static_cast<int>(H));
+    } else {  // reordered rows: the final dX rows go back in place (no-op otherwise)
+      const int sgrid = static_cast<int>(std::min<int64_t>((N + 7) / 8, static_cast<int64_t>(di.num_sms) * 8));
+      flce_dx_scatter_kernel<<<sgrid, 256, 0, stream>>>(lo, dX, perm, &ctrl->reordered, &ctrl->n_rows,
+                                                        static_cast<int>(N), static_cast<int>(H));
+    }
     prof_end(stream, slot);
     if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
   }
@@ -1266,6 +1293,7 @@ flce_status_t flce_policy_loss(const void* logits, int32_t dtype, int64_t ld, co
   a.status = d_status;
   a.inv_T = 1.0 / temperature;
   a.zs = static_cast<float>(1.0 / (LN2 * temperature));
+  a.zs_off = static_cast<double>(a.zs) * LN2 * temperature - 1.0;
   a.pol = policy_args(d_old_logp, d_advantage, d_ref_logp, clip_low, clip_high, kl_coef);
   a.ent_coef = entropy_coef;
   a.out_logp = d_logp;
@@ -1348,12 +1376,12 @@ flce_status_t flce_policy_forward_backward(const uint16_t* X, const uint16_t* W,
 
 size_t flce_policy_workspace_size(int64_t N, int64_t H, int64_t V, int32_t reorder) {
   if (check_sizes(N, H, V) != FLCE_OK) return 0;
-  return ws_layout(N, H, reorder != 0, wide_chunk(N, V)).total;
+  return wide_layout(N, H, V, reorder != 0).total;
 }
 
 size_t flce_distill_workspace_size(int64_t N, int64_t H, int64_t V, int32_t K, int32_t reorder) {
   if (check_sizes(N, H, V) != FLCE_OK || K <= 0 || K > DISTILL_MAX_K) return 0;
-  return ws_layout(N, H, reorder != 0, wide_chunk(N, V)).total + list_layout(N, K, 0).total;
+  return wide_layout(N, H, V, reorder != 0).total + list_layout(N, K, 0).total;
 }
 
 flce_status_t flce_distill_forward_backward(const uint16_t* X, const uint16_t* W, const int32_t* y, int64_t N,

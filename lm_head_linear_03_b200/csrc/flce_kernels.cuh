@@ -162,6 +162,8 @@ struct GemmArgs {
   const int* reordered;          // device word: 1 when the rows are reordered
   // pass 2 (one persistent launch over every chunk)
   int TM, HN;             // 256-row token tiles, 256-column hidden tiles
+  int KS;                 // dX items per tile: ranges of the chunk's vocabulary, each with a sum of its own (1: none)
+  float* dx_part;         // KS > 1: [KS][N][H] fp32 sums, joined by flce_dx_join_kernel
   int HW;                 // dW items per vocabulary tile: hidden tiles in pairs, the last alone when HN is odd
   int dw_lead;            // active k-blocks a paired dW item runs on its first half alone (see the issuer)
   int C;                  // vocabulary chunks
@@ -309,6 +311,36 @@ __device__ __forceinline__ void epi_lse_tile(const GemmArgs& a, uint32_t taddr, 
     }
     st.run_l = st.run_l * ex2_approx(st.run_m - new_m) + ((acc0 + acc1) + (acc2 + acc3));
     st.run_m = new_m;
+  }
+}
+
+// One vocabulary range's share of dX, added up over the chunks in fp32.  Each
+// thread holds a row: 128 contiguous bytes of it per slice, whole sectors.  The
+// sum of the chunk before was written by another SM, behind the counter this
+// item has waited for: it is read past L1.
+__device__ __forceinline__ void epi_dx_part(const GemmArgs& a, bool first_chunk, int ks, uint32_t taddr, int row0,
+                                            int nb, int row_local) {
+  const int row = row0 + row_local;
+  float* dst = a.dx_part + (static_cast<size_t>(ks) * a.N + min(row, a.N - 1)) * a.H;
+#pragma unroll 1
+  for (int c = 0; c < BN / 32; ++c) {
+    uint32_t r[32];
+    tmem_ld32(taddr + c * 32, r);
+    tmem_ld_wait();
+    const int col = nb * BN + c * 32;
+#pragma unroll
+    for (int t = 0; t < 32; t += 4) {
+      if (row < a.N && col + t < a.H) {  // H is a multiple of 8
+        float4* p = reinterpret_cast<float4*>(dst + col + t);
+        float4 v = make_float4(__uint_as_float(r[t]), __uint_as_float(r[t + 1]), __uint_as_float(r[t + 2]),
+                               __uint_as_float(r[t + 3]));
+        if (!first_chunk) {
+          const float4 o = __ldcg(p);
+          v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+        }
+        *p = v;
+      }
+    }
   }
 }
 
@@ -932,6 +964,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
 enum : int { ITEM_GRAD = 0, ITEM_DW = 1, ITEM_DX = 2 };
 
 struct Item {
+  int ks;             // dX: which of the KS vocabulary ranges
   int kind, c, a, b;  // G: (tm, vb)  dW: (vm, hidden tile pair)  dX: (tm, hn)
 };
 
@@ -940,10 +973,14 @@ __device__ __forceinline__ bool dw_paired(const GemmArgs& p, const Item& it) {
   return p.HW < p.HN && 2 * it.b + 1 < p.HN;
 }
 
+// First of the k-blocks of a dX item's vocabulary range (range ks + 1: its end).
+__device__ __forceinline__ int dx_range(const GemmArgs& p, int kblocks, int ks) {
+  return static_cast<int>(static_cast<long long>(kblocks) * ks / p.KS);
+}
 __device__ __forceinline__ int chunk_vtiles(const GemmArgs& p, int c) { return c == p.C - 1 ? p.VT_last : p.VTf; }
 
 __device__ __forceinline__ long long section_size(const GemmArgs& p, int c) {
-  long long n = static_cast<long long>(p.TM) * p.HN + static_cast<long long>(chunk_vtiles(p, c)) * p.HW;
+  long long n = static_cast<long long>(p.TM) * p.HN * p.KS + static_cast<long long>(chunk_vtiles(p, c)) * p.HW;
   if (c + 1 < p.C) n += static_cast<long long>(chunk_vtiles(p, c + 1)) * p.TM;
   return n;
 }
@@ -968,6 +1005,7 @@ __device__ __forceinline__ void grad_tile(const GemmArgs& p, int c, long long r,
 
 __device__ __forceinline__ Item decode_item(const GemmArgs& p, long long i) {
   Item it;
+  it.ks = 0;
   const long long g0 = static_cast<long long>(chunk_vtiles(p, 0)) * p.TM;
   if (i < g0) {
     it.kind = ITEM_GRAD;
@@ -987,13 +1025,18 @@ __device__ __forceinline__ Item decode_item(const GemmArgs& p, long long i) {
     r -= section_size(p, c);
     ++c;
   }
-  const long long nx = static_cast<long long>(p.TM) * p.HN;
+  const long long nx = static_cast<long long>(p.TM) * p.HN * p.KS;
   const long long nw = static_cast<long long>(chunk_vtiles(p, c)) * p.HW;
   it.c = c;
   if (r < nx) {
     it.kind = ITEM_DX;
-    it.a = static_cast<int>(r / p.HN);
-    it.b = static_cast<int>(r - static_cast<long long>(it.a) * p.HN);
+    const int per_row = p.HN * p.KS;
+    it.a = static_cast<int>(r / per_row);
+    it.b = static_cast<int>(r - static_cast<long long>(it.a) * per_row);
+    if (p.KS > 1) {
+      it.ks = it.b % p.KS;
+      it.b /= p.KS;
+    }
   } else if (r < nx + nw) {
     r -= nx;
     it.kind = ITEM_DW;
@@ -1124,7 +1167,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
         const int vcount = min(a.Vc, a.V - vbase);
         // G and dX tiles of a token tile whose rows are all ignored are skipped
         const bool skip = it.kind != ITEM_DW && a.tile_valid[it.a] == 0;
-        int kblocks;
+        int kblocks, kb0 = 0;
         if (skip) {
           kblocks = 0;
         } else if (it.kind == ITEM_GRAD) {
@@ -1135,6 +1178,10 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
                             a.timeout_ns);
         } else {
           kblocks = (vcount + BK - 1) / BK;
+          if (a.KS > 1) {
+            kb0 = dx_range(a, kblocks, it.ks);
+            kblocks = dx_range(a, kblocks, it.ks + 1);
+          }
           ok = wait_counter(a.g_row + it.a, g_row_target(it.c), abort_flag, a.timeout_ns);
         }
         if (!ok) {
@@ -1181,7 +1228,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
             if (a.tile_valid[kb / (CM / BK)] != 0) ok = fill_dw(kb, true, n0 + BN);
           continue;
         }
-        for (int kb = 0; kb < kblocks; ++kb) {
+        for (int kb = kb0; kb < kblocks; ++kb) {
           // dW: K runs over tokens; k-blocks of all-ignored token tiles add nothing
           if (it.kind == ITEM_DW && a.tile_valid[kb / (CM / BK)] == 0) continue;
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, a.timeout_ns)) {
@@ -1319,10 +1366,12 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
         }
         const int vcount = min(a.Vc, a.V - it.c * a.Vc);
         const bool skip = it.kind != ITEM_DW && a.tile_valid[it.a] == 0;
-        const int kblocks = skip                  ? 0
-                            : it.kind == ITEM_GRAD ? (a.H + BK - 1) / BK
-                            : it.kind == ITEM_DW   ? (a.N + BK - 1) / BK
-                                                   : (vcount + BK - 1) / BK;
+        int kblocks = skip                  ? 0
+                      : it.kind == ITEM_GRAD ? (a.H + BK - 1) / BK
+                      : it.kind == ITEM_DW   ? (a.N + BK - 1) / BK
+                                             : (vcount + BK - 1) / BK;
+        if (it.kind == ITEM_DX && a.KS > 1)
+          kblocks = dx_range(a, kblocks, it.ks + 1) - dx_range(a, kblocks, it.ks);
         const uint32_t idesc = it.kind == ITEM_GRAD ? ID_GRAD : it.kind == ITEM_DW ? ID_DW : ID_DX;
         const bool a_mn = it.kind == ITEM_DW;
         const bool b_mn = it.kind != ITEM_GRAD;
@@ -1402,10 +1451,10 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
       // wait for the previous readers (G) / writers (dX) of what this tile writes
       if (lane == 0) {
         if (it.kind == ITEM_GRAD && it.c > 0) {
-          ok = wait_counter(a.x_row + it.a, SIGNALS_PER_ITEM * it.c * a.HN, abort_flag, a.timeout_ns) &&
+          ok = wait_counter(a.x_row + it.a, SIGNALS_PER_ITEM * it.c * a.HN * a.KS, abort_flag, a.timeout_ns) &&
                wait_counter(a.w_col + it.b, SIGNALS_PER_ITEM * it.c * a.HN, abort_flag, a.timeout_ns);
         } else if (it.kind == ITEM_DX && it.c > 0) {
-          ok = wait_counter(a.x_row + it.a, SIGNALS_PER_ITEM * it.c * a.HN, abort_flag, a.timeout_ns);
+          ok = wait_counter(a.x_row + it.a, SIGNALS_PER_ITEM * it.c * a.HN * a.KS, abort_flag, a.timeout_ns);
         }
         if (ok) fence_proxy_async_global();
       }
@@ -1457,7 +1506,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
       if (skip) {
         // all rows ignored: nothing reads this tile's G rows; its dX rows are
         // zero, written once by the first chunk
-        if (it.kind == ITEM_DX && it.c == 0) epi_zero_tile(taddr, row0, it.b, row_local, es, &m.Hio);
+        if (it.kind == ITEM_DX && it.c == 0 && a.KS == 1) epi_zero_tile(taddr, row0, it.b, row_local, es, &m.Hio);
       } else if (it.kind == ITEM_GRAD) {
         epi_grad_tile<LIST>(a, vbase, taddr, row0, it.b, row_local, es, &m.Go, walk);
       } else if (it.kind == ITEM_DW) {
@@ -1466,6 +1515,8 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
           epi_dw_tile(vbase, taddr, row0, nt, row_local, es, &m.DWo);
         else
           epi_zero_tile(taddr, vbase + row0, nt, row_local, es, &m.DWo);
+      } else if (a.KS > 1) {
+        epi_dx_part(a, it.c == 0, it.ks, taddr, row0, it.b, row_local);
       } else {
         epi_dx_tile(a, it.c == 0, it.c == a.C - 1, taddr, row0, it.b, row_local, es, &m.Hio, &m.Loo, dx_final,
                     abort_flag, ok);
@@ -1630,6 +1681,36 @@ __global__ void __launch_bounds__(256)
     } else {
       for (int j = lane; j < h8; j += 32) d[j] = make_uint4(0u, 0u, 0u, 0u);
     }
+  }
+}
+
+// Joins the vocabulary ranges' shares of dX (KS > 1): their sum in range order,
+// rounded once, in the caller's row order; rows of all-ignored tiles, which no
+// item computed, are zero.  A thread takes eight columns.
+__global__ void __launch_bounds__(256)
+    flce_dx_join_kernel(const float* part, int KS, uint16_t* dX, const int* perm, const int* tile_valid, int N, int H) {
+  const int h8 = H / 8;
+  const long long total = static_cast<long long>(N) * h8;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const int r = static_cast<int>(i / h8), c = static_cast<int>(i - static_cast<long long>(r) * h8) * 8;
+    float v[8] = {};
+    if (tile_valid[r / CM] != 0) {
+#pragma unroll 4
+      for (int k = 0; k < KS; ++k) {
+        const float4* p = reinterpret_cast<const float4*>(part + (static_cast<size_t>(k) * N + r) * H + c);
+        const float4 x = p[0], y = p[1];
+        v[0] += x.x;
+        v[1] += x.y;
+        v[2] += x.z;
+        v[3] += x.w;
+        v[4] += y.x;
+        v[5] += y.y;
+        v[6] += y.z;
+        v[7] += y.w;
+      }
+    }
+    *reinterpret_cast<uint4*>(dX + static_cast<size_t>(perm[r]) * H + c) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
 }
 

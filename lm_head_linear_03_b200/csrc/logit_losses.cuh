@@ -362,6 +362,7 @@ struct LogitArgs {
   int* status;
   double inv_T;
   float zs;               // log2(e) / T
+  double zs_off;          // its rounding: zs / (log2(e) / T) - 1
   unsigned long long timeout_ns;
   // policy
   PolicyArgs pol;
@@ -766,8 +767,10 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
       // Log-probabilities as (z - m)/T - ln L: the difference first, so that a
       // row whose every logit is the type's lowest value still has one.
       const double m = static_cast<double>(w.m);
-      const double lnL = log(static_cast<double>(w.l));
       const double inv_l = 1.0 / static_cast<double>(w.l);
+      double lnL = log(static_cast<double>(w.l));
+      // zs is off by zs_off of itself: d ln L / d ln zs = ln 2 E[arg]
+      if (is_policy(LOSS)) lnL -= a.zs_off * LN2 * static_cast<double>(w.t) * inv_l;
       double total = 0.0;
       RowCoef c{w.m, 0.f, 0.f, 0.f, 0.f};
       if constexpr (is_policy(LOSS)) {

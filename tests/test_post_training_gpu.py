@@ -487,6 +487,28 @@ def test_heads_with_reordered_rows(reduction):
     assert_grad_close(_np(dW), G.T @ _np(X), "dW")
 
 
+@pytest.mark.parametrize("N,H,V", [(700, 64, 60000), (3, 1024, 30000), (260, 520, 20011), (513, 136, 70001)])
+def test_heads_on_both_workspaces(N, H, V):
+    """The heads' own workspace (wide chunks, dX in several vocabulary ranges,
+    one or more chunks) and the cross-entropy head's: both agree with the
+    oracle, in the caller's row order where rows are reordered too."""
+    F = _lib()
+    X, W, Z, y, old, adv, ref = _head(N, H, V, seed=N, ign=0.0 if N < 5 else 0.55)
+    d = _cuda(X, W, y, old, adv)
+    rloss, G, rlp, _, _ = O.policy_reference(Z, y, old, adv, None, 0.2, 0.28)
+    rX, rW = G @ _np(W), G.T @ _np(X)
+    sizes = (F.policy_workspace_size(N, H, V), F.policy_workspace_size(N, H, V, True), F.workspace_size(N, H))
+    for nbytes in sizes:
+        ws = torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+        loss, status, lp, dX, dW = F.policy_forward_backward(*d, clip_high=0.28, workspace=ws)
+        assert status.item() == 0
+        _close(_np(lp), rlp, 1e-4, "logp")
+        assert_grad_close(_np(dX), rX, "dX")
+        assert_grad_close(_np(dW), rW, "dW")
+        again = F.policy_forward_backward(*d, clip_high=0.28, workspace=ws)
+        assert torch.equal(again[3], dX) and torch.equal(again[4], dW)
+
+
 def test_policy_step_as_separate_calls():
     """Row losses, clipped_policy, weighted gradients: the same step as
     policy_forward_backward, and as policy_loss on the logits."""
