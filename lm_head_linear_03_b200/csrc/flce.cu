@@ -31,7 +31,7 @@ constexpr int VC = 2048;
 // 256000 6.7 against 7.5 ms.  G of 16 MB is 2 to 7% slower from 1024 rows on,
 // 128 MB the same as 64.
 constexpr int64_t WIDE_G_BYTES = 64ll << 20;
-constexpr int64_t WIDE_CHUNK = 65536;
+constexpr int64_t WIDE_CHUNK = 1 << 20;
 int wide_chunk(int64_t N, int64_t V) {
   const int64_t most = std::max<int64_t>(VC, std::min(WIDE_CHUNK, WIDE_G_BYTES / (2 * N)) / BN * BN);
   const int64_t chunks = (V + most - 1) / most;

@@ -1487,7 +1487,7 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
           eph ^= 1u << buf;
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (lane == 0 && it.c + 1 < a.C) {  // nothing waits for the last chunk's dW
           bulk_wait<0>();
           fence_proxy_async_global();
           red_release_gpu_add(a.w_col + it.a, 2);
@@ -1531,7 +1531,8 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(NUM_THREADS, 1
       eph ^= 1u << acc;
       acc ^= 1;
       // this warp's boxes have landed: count the tile as done for its readers
-      if (lane == 0) {
+      // (the last chunk's dW and dX have none: no wait for their stores)
+      if (lane == 0 && (it.kind == ITEM_GRAD || it.c + 1 < a.C)) {
         bulk_wait<0>();
         fence_proxy_async_global();
         if (it.kind == ITEM_GRAD) {
