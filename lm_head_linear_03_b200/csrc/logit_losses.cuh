@@ -610,35 +610,51 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
     // ---- what the row has besides its tiles, read ahead of its use
     float edge = edge_col >= 0 ? L::load(p.z + edge_col) : -INFINITY;
     PolicyIn pin{};
-    float zy = 0.f;
+    T zy_raw{};
     double scale = 1.0;
     if (tid < 32) {
       if (is_policy(LOSS)) pin = policy_load(a.pol, row);
-      zy = L::load(p.z + y);
+      zy_raw = p.z[y];
       scale = a.reduction == RED_MEAN ? inv_n
               : a.reduction == RED_NONE && a.row_scale ? static_cast<double>(a.row_scale[row]) : 1.0;
     }
     int* s_id = entries + parity * 4 * K1;
     float* s_c = reinterpret_cast<float*>(s_id + K1);
     float *s_z = s_c + K1, *s_u = s_z + K1;
-    if constexpr (!is_policy(LOSS)) {  // the teacher's entries, then the target
-      for (int k = tid; k < K1; k += LOGIT_THREADS) {
-        int id = y;
-        float u = -INFINITY;
-        if (k < a.K) {
-          const size_t at = static_cast<size_t>(row) * a.K + k;
-          id = a.ids[at];
-          if (id >= a.V) {
-            raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
-            id = -1;
-          }
-          if (id >= 0) u = load_as_f32(a.u, a.u_dtype, at);
-        }
-        s_id[k] = id < 0 ? -1 : id;
-        s_u[k] = u;
-        s_z[k] = id >= 0 && (rank == 0 || p.has(id)) ? L::load(p.z + id) : 0.f;
-      }
+    // The teacher's entries, then the target.  A thread's first one is read in
+    // three steps, each waited for only at the next: id and teacher logit here,
+    // the student's logit behind the first tile, its use behind the last.
+    auto teacher_id = [&](int k) { return k < a.K ? a.ids[static_cast<size_t>(row) * a.K + k] : y; };
+    auto teacher_u = [&](int k) {
+      return k < a.K ? load_as_f32(a.u, a.u_dtype, static_cast<size_t>(row) * a.K + k) : -INFINITY;
+    };
+    auto wanted = [&](int id) { return id >= 0 && (rank == 0 || p.has(id)); };
+    auto checked = [&](int id) {
+      if (id >= a.V) raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
+      return id < 0 || id >= a.V ? -1 : id;
+    };
+    int my_id = -1;
+    float my_u = -INFINITY;
+    T my_z{};
+    if (!is_policy(LOSS) && tid < K1) {
+      my_id = teacher_id(tid);
+      my_u = teacher_u(tid);
     }
+    auto read_entries = [&]() {
+      if (is_policy(LOSS)) return;
+      for (int k = tid; k < K1; k += LOGIT_THREADS) {
+        const int id = checked(k == tid ? my_id : teacher_id(k));
+        const float u = k == tid ? my_u : teacher_u(k);
+        s_id[k] = id;
+        s_u[k] = id < 0 ? -INFINITY : u;
+        if (k == tid) {
+          my_id = id;
+          if (wanted(id)) my_z = p.z[id];
+        } else {
+          s_z[k] = wanted(id) ? L::load(p.z + id) : 0.f;
+        }
+      }
+    };
 
     // ---- first walk: maximum and sums, online, each lane under its own maximum
     float top = edge;  // the largest logit as it stands
@@ -711,7 +727,10 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
         fold_tile(Flag<true>{}, size);
       else
         fold_tile(Flag<false>{}, size);
+      if (k == 0) read_entries();
     }
+    if (p.tiles == 0) read_entries();
+    if (!is_policy(LOSS) && tid < K1) s_z[tid] = wanted(my_id) ? L::load(&my_z) : 0.f;
     // the lanes under the warp's maximum
     {
       float lo, hi;
@@ -771,6 +790,7 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
       double lnL = log(static_cast<double>(w.l));
       // zs is off by zs_off of itself: d ln L / d ln zs = ln 2 E[arg]
       if (is_policy(LOSS)) lnL -= a.zs_off * LN2 * static_cast<double>(w.t) * inv_l;
+      const float zy = L::load(&zy_raw);
       double total = 0.0;
       RowCoef c{w.m, 0.f, 0.f, 0.f, 0.f};
       if constexpr (is_policy(LOSS)) {
@@ -861,14 +881,18 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
         f32x2_split(dense2(f32x2(x, x)), lo, hi);
         return lo;
       };
-      // what is subtracted at column id: equal ids add up, and each writes the same sum
+      // what is subtracted at column id: equal ids add up
       auto sparse = [&](int id) {
         if (is_policy(LOSS)) return id == y ? c.c : 0.f;
         float sum = 0.f;
-        for (int k = 0; k < K1; ++k)
-          if (s_id[k] == id) sum += s_c[k];
+#pragma unroll 4
+        for (int k = 0; k < K1; ++k) sum += s_id[k] == id ? s_c[k] : 0.f;
         return sum;
       };
+      if constexpr (!is_policy(LOSS)) {  // every entry's, in place of the teacher's logits (equal ids: the same sum)
+        for (int k = tid; k < K1; k += LOGIT_THREADS) s_u[k] = sparse(s_id[k]);
+        __syncthreads();
+      }
       if (edge_col >= 0) p.g[edge_col] = L::round(dense(edge) - sparse(edge_col));
       for (int k = p.tiles - 1; k >= 0; --k) {
         const int at = p.tile_at(k, warp), size = p.tile_size(at);
@@ -904,7 +928,7 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
           __syncwarp();
           for (int i = lane; i < K1; i += 32) {
             const int id = s_id[i];
-            if (id >= col && id < end) reinterpret_cast<T*>(tile)[id - col] = L::round(dense(s_z[i]) - sparse(id));
+            if (id >= col && id < end) reinterpret_cast<T*>(tile)[id - col] = L::round(dense(s_z[i]) - s_u[i]);
           }
         }
         if (p.vec_out) {
