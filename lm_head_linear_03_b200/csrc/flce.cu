@@ -926,14 +926,14 @@ constexpr int MAX_FITS = 256;
 LogitFit g_fit[MAX_FITS];
 int g_fits = 0;
 
-template <typename T, int LOSS>
-cudaError_t launch_logit_type(const LogitArgs& a, int num_sms, int dev, size_t smem, cudaStream_t stream) {
-  const auto kernel = flce_logit_loss_kernel<T, LOSS>;
-  const int cs = logit_cluster(a.N, a.V, sizeof(T), num_sms);
-  smem += LOGIT_RING_BYTES;
+template <typename T, int LOSS, int THREADS>
+cudaError_t launch_logit_shape(const LogitArgs& a, int cs, int dev, size_t smem, cudaStream_t stream) {
+  constexpr size_t RING = THREADS / 32 * WARP_RING_BYTES;
+  const auto kernel = flce_logit_loss_kernel<T, LOSS, THREADS>;
+  smem += RING;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(cs), 1, 1);
-  cfg.blockDim = dim3(LOGIT_THREADS, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -952,7 +952,7 @@ cudaError_t launch_logit_type(const LogitArgs& a, int num_sms, int dev, size_t s
         fit = g_fit[k].clusters;
     if (!fit) {
       cudaError_t e;
-      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LOGIT_RING_BYTES + 32 * (DISTILL_MAX_K + 1))) !=
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING + 32 * (DISTILL_MAX_K + 1))) !=
               cudaSuccess ||
           (e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg)) != cudaSuccess)
         return e;
@@ -962,6 +962,39 @@ cudaError_t launch_logit_type(const LogitArgs& a, int num_sms, int dev, size_t s
   }
   cfg.gridDim = dim3(static_cast<unsigned>(std::min(a.N, fit) * cs), 1, 1);
   return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// Threads of a CTA.  Smaller CTAs put more rows on an SM, which hide one
+// another's exchanges, as long as the rows under way fit in L2: half CTAs up to
+// 100 KB a row, single warps up to 24 KB.  The count with the least rounds of
+// rows times what a row costs a warp, in tiles, the exchanges as one more.
+// Measured (bf16 policy loss, 256 threads / 128 / 32): 8192 x 32064 268 / 250 us,
+// 16384 x 4096 271 / 152 / 108 us, 16384 x 119 267 / 142 / 69 us.
+int logit_threads(int64_t N, int64_t row_bytes, int cs, int num_sms) {
+  if (cs > 1) return LOGIT_THREADS;
+  const int64_t tiles = row_bytes / (TILE_CHUNKS * 16) + 1;
+  int best = LOGIT_THREADS;
+  int64_t least = INT64_MAX;
+  for (int t : {LOGIT_THREADS, LOGIT_THREADS / 2, 32}) {
+    if ((t < LOGIT_THREADS && row_bytes > 100 * 1024) || (t == 32 && row_bytes > 24 * 1024)) continue;
+    const int64_t rows = static_cast<int64_t>(num_sms) * 2 * LOGIT_THREADS / t, warps = t / 32;
+    const int64_t cost = ((N + rows - 1) / rows) * (1 + (tiles + warps - 1) / warps);
+    if (cost < least) {
+      least = cost;
+      best = t;
+    }
+  }
+  return best;
+}
+
+template <typename T, int LOSS>
+cudaError_t launch_logit_type(const LogitArgs& a, int num_sms, int dev, size_t smem, cudaStream_t stream) {
+  const int cs = logit_cluster(a.N, a.V, sizeof(T), num_sms);
+  switch (logit_threads(a.N, static_cast<int64_t>(a.V) * sizeof(T), cs, num_sms)) {
+    case 32: return launch_logit_shape<T, LOSS, 32>(a, cs, dev, smem, stream);
+    case LOGIT_THREADS / 2: return launch_logit_shape<T, LOSS, LOGIT_THREADS / 2>(a, cs, dev, smem, stream);
+    default: return launch_logit_shape<T, LOSS, LOGIT_THREADS>(a, cs, dev, smem, stream);
+  }
 }
 
 template <int LOSS>
@@ -980,7 +1013,7 @@ flce_status_t enqueue_logit_loss(LogitArgs& a, int loss, int32_t dtype, uint8_t*
   const CeLayout L = ce_ws_layout(a.N);
   const flce_status_t s = begin_rows(a.y, a.N, a.ignore_index, ws, L, a.status, &a.valid, &a.ticket, stream);
   if (s != FLCE_OK) return s;
-  a.row_acc = reinterpret_cast<double*>(ws + L.row_acc);
+  a.sums = reinterpret_cast<double*>(ws + L.row_acc);
   a.timeout_ns = DEFAULT_TIMEOUT_NS;
   const size_t smem = is_policy(loss) ? 0 : 2 * 16 * (static_cast<size_t>(a.K) + 1);
   size_t slot;

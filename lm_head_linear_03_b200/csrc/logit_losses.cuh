@@ -170,8 +170,8 @@ __device__ __forceinline__ int count_rows(const RowCounts& r) {
   return n;
 }
 
-// The last block to finish adds the rows' contributions in row order: a fixed
-// tree over a fixed assignment, in fp64.
+// The last block to finish adds the blocks' sums: a fixed tree over a fixed
+// assignment, in fp64.
 template <int THREADS>
 __device__ __forceinline__ double ordered_sum(const double* v, int n, double* scratch) {
   double s = 0.0;
@@ -357,7 +357,7 @@ struct LogitArgs {
   const float* row_scale;
   RowCounts valid;
   unsigned int* ticket;
-  double* row_acc;        // [N]
+  double* sums;           // [clusters], at most N
   float* loss;
   int* status;
   double inv_T;
@@ -426,18 +426,17 @@ struct Flag {  // a compile-time truth value to pass to a lambda
   static constexpr bool value = B;
 };
 
-constexpr int LOGIT_THREADS = 256;
-constexpr int LOGIT_WARPS = LOGIT_THREADS / 32;
+constexpr int LOGIT_THREADS = 256;  // of a CTA; fewer for short rows (see the launch)
 constexpr int LOGIT_MAX_CLUSTER = 8;
 constexpr int TILE_CHUNKS = 256;  // 16-byte chunks of a warp's tile (4 KB), eight per lane
 constexpr int TILE_STAGES = 3;    // tiles per warp in shared memory
-constexpr int LOGIT_RING_BYTES = LOGIT_WARPS * TILE_STAGES * TILE_CHUNKS * 16;
+constexpr int WARP_RING_BYTES = TILE_STAGES * TILE_CHUNKS * 16;
 
 // Where row `row` lies, and which of it is CTA `rank`'s part.  Bulk copies move
 // 16-byte chunks on 16-byte boundaries: the up to 2 * (EPC - 1) elements in
 // front of the first and behind the last boundary ("edges") are held one per
 // thread by the cluster's first CTA.
-template <typename T>
+template <typename T, int WARPS>
 struct RowPart {
   static constexpr int EPC = LogitTraits<T>::EPC;
   const T* z;
@@ -445,7 +444,7 @@ struct RowPart {
   int head, edges;  // elements before the first boundary, elements outside chunks
   int n;            // this CTA's chunks
   int col0;         // column of the first one
-  int tiles;        // tiles of the calling warp: those j < ceil(n / TILE_CHUNKS) with j % LOGIT_WARPS == warp
+  int tiles;        // tiles of the calling warp: those j < ceil(n / TILE_CHUNKS) with j % WARPS == warp
   bool vec_out;     // the gradient row shares the logits' alignment
   __device__ RowPart(const LogitArgs& a, int row, int rank, int cs, int warp) {
     z = static_cast<const T*>(a.z) + static_cast<long long>(row) * a.ld;
@@ -459,12 +458,12 @@ struct RowPart {
     n = min(per, chunks - c0);
     col0 = head + c0 * EPC;
     const int all = (n + TILE_CHUNKS - 1) / TILE_CHUNKS;
-    tiles = all > warp ? (all - warp + LOGIT_WARPS - 1) / LOGIT_WARPS : 0;
+    tiles = all > warp ? (all - warp + WARPS - 1) / WARPS : 0;
     vec_out = g && ((reinterpret_cast<uintptr_t>(g) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
   }
   __device__ bool has(int id) const { return id >= col0 && id < col0 + n * EPC; }
   // first chunk and chunk count of the calling warp's k-th tile
-  __device__ int tile_at(int k, int warp) const { return (k * LOGIT_WARPS + warp) * TILE_CHUNKS; }
+  __device__ int tile_at(int k, int warp) const { return (k * WARPS + warp) * TILE_CHUNKS; }
   __device__ int tile_size(int at) const { return min(TILE_CHUNKS, n - at); }
   __device__ int edge_col(const LogitArgs& a, int rank, int tid) const {
     return rank == 0 && tid < edges ? (tid < head ? tid : a.V - edges + tid) : -1;
@@ -494,20 +493,21 @@ __device__ __forceinline__ bool row_counts(const LogitArgs& a, int y) {
 // maxima and warp 0 of each CTA the sums, in a fixed order, so all CTAs find the
 // same totals.  Warp 0 turns them into the row's outputs (first CTA) and the
 // gradient's coefficients.
-template <typename T, int LOSS>
-__global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const LogitArgs a) {
+template <typename T, int LOSS, int THREADS>
+__global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_logit_loss_kernel(const LogitArgs a) {
   using L = LogitTraits<T>;
   constexpr int EPC = L::EPC;
   constexpr int LANE_CHUNKS = TILE_CHUNKS / 32;
+  constexpr int WARPS = THREADS / 32;
   extern __shared__ __align__(128) uint8_t dyn_tiles[];
   const int K1 = is_policy(LOSS) ? 0 : a.K + 1;
   // the warps' rings, then twice (for two rows) the sparse entries: vocabulary
   // ids (-1: none), coefficients subtracted there, the student's logits, the teacher's
-  int* entries = reinterpret_cast<int*>(dyn_tiles + LOGIT_RING_BYTES);
-  __shared__ float4 rec[2][LOGIT_MAX_CLUSTER * LOGIT_WARPS];
+  int* entries = reinterpret_cast<int*>(dyn_tiles + WARPS * WARP_RING_BYTES);
+  __shared__ float4 rec[2][LOGIT_MAX_CLUSTER * WARPS];
   __shared__ RowCoef coefs[2];
-  __shared__ double dsum[LOGIT_WARPS];
-  __shared__ uint64_t bars[LOGIT_WARPS * TILE_STAGES];
+  __shared__ double dsum[WARPS];
+  __shared__ uint64_t bars[WARPS * TILE_STAGES];
   __shared__ int abort_flag;
   __shared__ bool is_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -524,22 +524,27 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
   const int n_valid = count_rows(a.valid);
   const double inv_n = n_valid > 0 ? 1.0 / static_cast<double>(n_valid) : 0.0;
   const int walks = a.g ? 2 : 1;
-  auto next_counting = [&](int r) {
-    while (r < a.N && !row_counts(a, a.y[r])) r += clusters;
-    return r;
-  };
-
   // ---- the warp's ring: tiles are issued and used in the same order
   const int first = blockIdx.x / cs;
-  int ahead = next_counting(first);  // row of the next tile to issue
-  RowPart<T> ap(a, min(ahead, a.N - 1), rank, cs, warp);
+  // Targets are read a row ahead of the question whether the row counts.
+  auto target = [&](int r) { return r < a.N ? a.y[r] : a.ignore_index; };
+  int ahead = first;  // row of the next tile to issue; `then` follows it
+  while (ahead < a.N && !row_counts(a, a.y[ahead])) ahead += clusters;
+  int then = ahead + clusters, then_y = target(then);
+  RowPart<T, WARPS> ap(a, min(ahead, a.N - 1), rank, cs, warp);
   int ahead_k = 0;                   // its number in the row's 2 * tiles (or tiles) ones
   int in_stage = 0;
   auto issue = [&]() {
     while (ahead < a.N && ahead_k == walks * ap.tiles) {
-      ahead = next_counting(ahead + clusters);
+      while (then < a.N && !row_counts(a, then_y)) {
+        then += clusters;
+        then_y = target(then);
+      }
+      ahead = then;
+      then += clusters;
+      then_y = target(then);
       ahead_k = 0;
-      if (ahead < a.N) ap = RowPart<T>(a, ahead, rank, cs, warp);
+      if (ahead < a.N) ap = RowPart<T, WARPS>(a, ahead, rank, cs, warp);
     }
     if (ahead >= a.N || *const_cast<volatile int*>(&abort_flag)) return;
     const bool again = ahead_k >= ap.tiles;
@@ -581,14 +586,16 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
   const float none = is_policy(LOSS) ? LOGIT_NONE : -INFINITY;
   const uint64_t zs2 = f32x2(a.zs, a.zs), one2 = f32x2(LOG2E, LOG2E);
   int parity = 0;
+  double sum = 0.0;  // thread 0: the losses of this CTA's rows, in their order
+  int next_y = target(first);
   for (int row = first; row < a.N; row += clusters) {
-    const RowPart<T> p(a, row, rank, cs, warp);
+    const int y = next_y;
+    next_y = target(row + clusters);
+    const RowPart<T, WARPS> p(a, row, rank, cs, warp);
     const int edge_col = p.edge_col(a, rank, tid);
-    const int y = a.y[row];
     if (!row_counts(a, y)) {
       if (rank == 0 && tid == 0) {
         if (y != a.ignore_index) raise_status(a.status, ST_TARGET_OUT_OF_RANGE);
-        a.row_acc[row] = 0.0;
         if constexpr (is_policy(LOSS)) {
           a.out_logp[row] = a.out_entropy[row] = a.out_kl[row] = 0.f;
         } else if (a.out_rows) {
@@ -598,9 +605,9 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
       if (p.g) {
         if ((reinterpret_cast<uintptr_t>(p.g + p.col0) & 15) == 0) {
           uint4* gv = reinterpret_cast<uint4*>(p.g + p.col0);
-          for (int c = tid; c < p.n; c += LOGIT_THREADS) st_l2hint_v4(gv + c, make_uint4(0u, 0u, 0u, 0u), last);
+          for (int c = tid; c < p.n; c += THREADS) st_l2hint_v4(gv + c, make_uint4(0u, 0u, 0u, 0u), last);
         } else {
-          for (int e = tid; e < p.n * EPC; e += LOGIT_THREADS) p.g[p.col0 + e] = L::round(0.f);
+          for (int e = tid; e < p.n * EPC; e += THREADS) p.g[p.col0 + e] = L::round(0.f);
         }
         if (edge_col >= 0) p.g[edge_col] = L::round(0.f);
       }
@@ -641,8 +648,8 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
       my_u = teacher_u(tid);
     }
     auto read_entries = [&]() {
-      if (is_policy(LOSS)) return;
-      for (int k = tid; k < K1; k += LOGIT_THREADS) {
+      if constexpr (!is_policy(LOSS)) {
+      for (int k = tid; k < K1; k += THREADS) {
         const int id = checked(k == tid ? my_id : teacher_id(k));
         const float u = k == tid ? my_u : teacher_u(k);
         s_id[k] = id;
@@ -653,6 +660,7 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
         } else {
           s_z[k] = wanted(id) ? L::load(p.z + id) : 0.f;
         }
+      }
       }
     };
 
@@ -757,14 +765,14 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
       __syncthreads();
     } else {
       if (lane < cs)
-        st_cluster_f4(mapa_shared(smem_u32(&rec[parity][rank * LOGIT_WARPS + warp]), lane),
+        st_cluster_f4(mapa_shared(smem_u32(&rec[parity][rank * WARPS + warp]), lane),
                       make_float4(w.m, w.l, w.t, top));
       cluster_sync_all();
     }
 
     // ---- the row's totals and scalars
     if (warp == 0) {
-      const int records = cs * LOGIT_WARPS;
+      const int records = cs * WARPS;
       w = RowStat{-FLT_MAX, 0.f, 0.f};
       top = -INFINITY;
       for (int r = lane; r < records; r += 32) {
@@ -849,7 +857,7 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
       }
       if (lane == 0) {
         coefs[parity] = c;
-        if (rank == 0) a.row_acc[row] = a.reduction == RED_MEAN ? total : total * scale;
+        sum += a.reduction == RED_MEAN ? total : total * scale;
       }
     }
 
@@ -890,7 +898,7 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
         return sum;
       };
       if constexpr (!is_policy(LOSS)) {  // every entry's, in place of the teacher's logits (equal ids: the same sum)
-        for (int k = tid; k < K1; k += LOGIT_THREADS) s_u[k] = sparse(s_id[k]);
+        for (int k = tid; k < K1; k += THREADS) s_u[k] = sparse(s_id[k]);
         __syncthreads();
       }
       if (edge_col >= 0) p.g[edge_col] = L::round(dense(edge) - sparse(edge_col));
@@ -963,13 +971,14 @@ __global__ void __launch_bounds__(LOGIT_THREADS, 2) flce_logit_loss_kernel(const
   // the loss, by the last cluster to finish
   if (rank != 0) return;
   if (tid == 0) {
+    a.sums[first] = sum;
     __threadfence();
     is_last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(clusters - 1);
   }
   __syncthreads();
   if (!is_last) return;
   __threadfence();
-  const double t = ordered_sum<LOGIT_THREADS>(a.row_acc, a.N, dsum);
+  const double t = ordered_sum<THREADS>(a.sums, clusters, dsum);
   if (tid == 0) *a.loss = static_cast<float>(a.reduction == RED_MEAN ? t * inv_n : t);
 }
 
