@@ -379,44 +379,22 @@ struct LogitArgs {
   float* out_rows;        // [N] or null
 };
 
-// A row's running statistics: max of z, sum of e = 2^((z - m) zs), and for the
-// policy loss the first moment sum e (z - m) zs, for DISTILL2 the sum of
-// 2^((z - m) log2 e).
+// A row's running statistics under a reference m, which is the maximum to
+// within RAISE in the exponent: sum of e = 2^((z - m) zs), and for the policy loss
+// the first moment sum e (z - m) zs, for DISTILL2 the sum of 2^((z - m) log2 e).
 struct RowStat {
   float m, l, t;
 };
-
-template <int LOSS>
-__device__ __forceinline__ void stat_add(RowStat& s, float z, float zs) {
-  if (z > s.m) {  // move to the new maximum
-    const float d = (s.m - z) * zs, f = ex2_approx(d);
-    if constexpr (is_policy(LOSS)) s.t = f * (s.t + s.l * fmaxf(d, NEG_BIG));
-    if constexpr (LOSS == LOSS_DISTILL2) s.t *= ex2_approx((s.m - z) * LOG2E);
-    s.l *= f;
-    s.m = z;
-  }
-  const float d = (z - s.m) * zs, e = ex2_approx(d);
-  s.l += e;
-  if constexpr (is_policy(LOSS)) s.t += e * fmaxf(d, NEG_BIG);
-  if constexpr (LOSS == LOSS_DISTILL2) s.t += ex2_approx((z - s.m) * LOG2E);
-}
-
-template <int LOSS>
-__device__ __forceinline__ void stat_merge(RowStat& s, const RowStat& o, float zs) {
-  const float m = fmaxf(s.m, o.m);
-  const float d1 = (s.m - m) * zs, d2 = (o.m - m) * zs;
-  const float f1 = ex2_approx(d1), f2 = ex2_approx(d2);
-  if constexpr (is_policy(LOSS))
-    s.t = f1 * (s.t + s.l * fmaxf(d1, NEG_BIG)) + f2 * (o.t + o.l * fmaxf(d2, NEG_BIG));
-  if constexpr (LOSS == LOSS_DISTILL2)
-    s.t = s.t * ex2_approx((s.m - m) * LOG2E) + o.t * ex2_approx((o.m - m) * LOG2E);
-  s.l = s.l * f1 + o.l * f2;
-  s.m = m;
-}
+// How far a logit may lie above the reference, in the exponent, before the
+// reference moves: rarely, because each move rounds the sums.
+constexpr float RAISE = 60.f;
+// Mean relative error of the hardware's 2^x over arguments below -1, measured:
+// it does not average out of a sum of exponentials.
+constexpr double EX2_BIAS = -5.0e-8;
 
 // What the gradient needs of a row.
 struct RowCoef {
-  float m;       // the row's maximum
+  float m;       // the row's reference
   float a, b;    // dense part: e (a + b arg), or a e + b e1 with two softmaxes
   float c, zy;   // policy: subtracted at the target, and the logit there
 };
@@ -488,11 +466,11 @@ __device__ __forceinline__ bool row_counts(const LogitArgs& a, int y) {
 // waits for no other warp.  Gradient tiles are written in place of the logits
 // and leave by bulk copies too.
 //
-// Statistics: lanes fold under maxima of their own, warps write one record each
-// into every CTA of the cluster, and behind one barrier every warp merges the
-// maxima and warp 0 of each CTA the sums, in a fixed order, so all CTAs find the
-// same totals.  Warp 0 turns them into the row's outputs (first CTA) and the
-// gradient's coefficients.
+// Statistics: every warp folds its elements under a reference near its maximum
+// and writes one record into every CTA of the cluster; behind one barrier warp 0
+// of each CTA merges the records in a fixed order, so all CTAs find the same
+// totals, and turns them into the row's outputs (first CTA) and the gradient's
+// coefficients.
 template <typename T, int LOSS, int THREADS>
 __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_logit_loss_kernel(const LogitArgs a) {
   using L = LogitTraits<T>;
@@ -664,12 +642,46 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
       }
     };
 
-    // ---- first walk: maximum and sums, online, each lane under its own maximum
-    float top = edge;  // the largest logit as it stands
-    RowStat w{is_policy(LOSS) ? LOGIT_LOWEST : -FLT_MAX, 0.f, 0.f};
+    // ---- first walk: the sums, each warp under a reference of its own
+    float top = edge;  // this lane's largest logit as it stands
     if (is_policy(LOSS)) edge = edge_col >= 0 ? lifted(edge) : none;
-    if (edge_col >= 0) stat_add<LOSS>(w, edge, a.zs);
-    uint64_t l2 = f32x2(w.l, 0.f), t2 = f32x2(w.t, 0.f);  // two partial sums each
+    float ref = is_policy(LOSS) ? LOGIT_LOWEST : -FLT_MAX;  // the warp's reference
+    uint64_t l2 = 0ull, t2 = 0ull;                          // this lane's sums, in two parts each
+    auto raise = [&](float lane_top) {  // the reference, where some lane's logits need it
+      if (!__any_sync(0xffffffffu, (lane_top - ref) * a.zs > RAISE)) return;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) lane_top = fmaxf(lane_top, __shfl_xor_sync(0xffffffffu, lane_top, s));
+      const float d = (ref - lane_top) * a.zs, f = ex2_approx(d);
+      const uint64_t f2 = f32x2(f, f);
+      if constexpr (is_policy(LOSS)) {
+        const float df = fmaxf(d, NEG_BIG);
+        t2 = mul2(f2, fma2(l2, f32x2(df, df), t2));
+      }
+      if constexpr (LOSS == LOSS_DISTILL2) {
+        const float f1 = ex2_approx((ref - lane_top) * LOG2E);
+        t2 = mul2(t2, f32x2(f1, f1));
+      }
+      l2 = mul2(l2, f2);
+      ref = lane_top;
+    };
+    auto fold = [&](uint64_t x) {
+      const uint64_t d0 = add2(x, f32x2(-ref, -ref));
+      uint64_t d = mul2(d0, zs2);
+      float lo, hi;
+      f32x2_split(d, lo, hi);
+      if constexpr (is_policy(LOSS) && !L::CLAMPS) {  // finite, so that a probability of 0 adds 0 to the entropy
+        lo = max_nan(lo, NEG_BIG);
+        hi = max_nan(hi, NEG_BIG);
+        d = f32x2(lo, hi);
+      }
+      const uint64_t e = f32x2(ex2_approx(lo), ex2_approx(hi));
+      l2 = add2(l2, e);
+      if constexpr (is_policy(LOSS)) t2 = fma2(e, d, t2);
+      if constexpr (LOSS == LOSS_DISTILL2) {
+        f32x2_split(mul2(d0, one2), lo, hi);
+        t2 = add2(t2, f32x2(ex2_approx(lo), ex2_approx(hi)));
+      }
+    };
     auto fold_tile = [&](auto full, int size) {
       auto has = [&](int u) { return decltype(full)::value || u * 32 + lane < size; };
       uint4 v[LANE_CHUNKS];
@@ -686,39 +698,7 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
         if (has(u)) L::max_add(vmax, v[u]);
       const float tile_top = L::max_get(vmax);
       top = fmaxf(top, tile_top);
-      if (tile_top > w.m) {
-        const float d = (w.m - tile_top) * a.zs, f = ex2_approx(d);
-        const uint64_t f2 = f32x2(f, f);
-        if constexpr (is_policy(LOSS)) {
-          const float df = fmaxf(d, NEG_BIG);
-          t2 = mul2(f2, fma2(l2, f32x2(df, df), t2));
-        }
-        if constexpr (LOSS == LOSS_DISTILL2) {
-          const float f1 = ex2_approx((w.m - tile_top) * LOG2E);
-          t2 = mul2(t2, f32x2(f1, f1));
-        }
-        l2 = mul2(l2, f2);
-        w.m = tile_top;
-      }
-      const uint64_t neg_m2 = f32x2(-w.m, -w.m);
-      auto fold = [&](uint64_t x) {
-        const uint64_t d0 = add2(x, neg_m2);
-        uint64_t d = mul2(d0, zs2);
-        float lo, hi;
-        f32x2_split(d, lo, hi);
-        if constexpr (is_policy(LOSS) && !L::CLAMPS) {  // finite, so that a probability of 0 adds 0 to the entropy
-          lo = max_nan(lo, NEG_BIG);
-          hi = max_nan(hi, NEG_BIG);
-          d = f32x2(lo, hi);
-        }
-        const uint64_t e = f32x2(ex2_approx(lo), ex2_approx(hi));
-        l2 = add2(l2, e);
-        if constexpr (is_policy(LOSS)) t2 = fma2(e, d, t2);
-        if constexpr (LOSS == LOSS_DISTILL2) {
-          f32x2_split(mul2(d0, one2), lo, hi);
-          t2 = add2(t2, f32x2(ex2_approx(lo), ex2_approx(hi)));
-        }
-      };
+      raise(tile_top);
 #pragma unroll
       for (int u = 0; u < LANE_CHUNKS; ++u) {
         if (has(u)) {
@@ -739,26 +719,21 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
     }
     if (p.tiles == 0) read_entries();
     if (!is_policy(LOSS) && tid < K1) s_z[tid] = wanted(my_id) ? L::load(&my_z) : 0.f;
-    // the lanes under the warp's maximum
+    raise(edge);
+    fold(f32x2(edge, none));
+    RowStat w{ref, 0.f, 0.f};
     {
       float lo, hi;
       f32x2_split(l2, lo, hi);
       w.l = lo + hi;
       f32x2_split(t2, lo, hi);
       w.t = lo + hi;
-      RowStat o{w.m, 0.f, 0.f};
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) {
-        o.m = fmaxf(o.m, __shfl_xor_sync(0xffffffffu, o.m, s));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-      }
-      stat_merge<LOSS>(o, w, a.zs);
-      w = o;
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) {
         w.l += __shfl_xor_sync(0xffffffffu, w.l, s);
         w.t += __shfl_xor_sync(0xffffffffu, w.t, s);
       }
+      top = __any_sync(0xffffffffu, top > -INFINITY) ? 1.f : 0.f;  // some logit is above -infinity
     }
     if (cs == 1) {
       if (lane == 0) rec[parity][warp] = make_float4(w.m, w.l, w.t, top);
@@ -772,38 +747,45 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
 
     // ---- the row's totals and scalars
     if (warp == 0) {
+      // The records under the largest reference, in fp64: a rounded factor
+      // would put the same error on a whole warp's sum.
       const int records = cs * WARPS;
-      w = RowStat{-FLT_MAX, 0.f, 0.f};
-      top = -INFINITY;
+      float ref_max = -FLT_MAX;
+      for (int r = lane; r < records; r += 32) ref_max = fmaxf(ref_max, rec[parity][r].x);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) ref_max = fmaxf(ref_max, __shfl_xor_sync(0xffffffffu, ref_max, s));
+      double sum_l = 0.0, sum_t = 0.0;
+      top = 0.f;
       for (int r = lane; r < records; r += 32) {
         const float4 v = rec[parity][r];
-        stat_merge<LOSS>(w, RowStat{v.x, v.y, v.z}, a.zs);
+        const double gap = static_cast<double>(v.x) - static_cast<double>(ref_max);
+        const double d = fmax(gap * static_cast<double>(a.zs), static_cast<double>(NEG_BIG)), f = exp2(d);
+        sum_l += f * static_cast<double>(v.y);
+        if constexpr (is_policy(LOSS)) sum_t += f * (static_cast<double>(v.z) + d * static_cast<double>(v.y));
+        if constexpr (LOSS == LOSS_DISTILL2)
+          sum_t += exp2(fmax(gap * static_cast<double>(LOG2E), static_cast<double>(NEG_BIG))) * static_cast<double>(v.z);
         top = fmaxf(top, v.w);
       }
-      RowStat o{w.m, 0.f, 0.f};
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) o.m = fmaxf(o.m, __shfl_xor_sync(0xffffffffu, o.m, s));
-      stat_merge<LOSS>(o, w, a.zs);
-      w = o;
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) {
-        w.l += __shfl_xor_sync(0xffffffffu, w.l, s);
-        w.t += __shfl_xor_sync(0xffffffffu, w.t, s);
+        sum_l += __shfl_xor_sync(0xffffffffu, sum_l, s);
+        sum_t += __shfl_xor_sync(0xffffffffu, sum_t, s);
       }
-      if (is_policy(LOSS) && !__any_sync(0xffffffffu, top > -INFINITY)) w.l = 0.f;  // every logit is -infinity: NaN
+      sum_l *= 1.0 - EX2_BIAS;
+      if (is_policy(LOSS) && !__any_sync(0xffffffffu, top > 0.f)) sum_l = 0.0;  // every logit is -infinity: NaN
       // Log-probabilities as (z - m)/T - ln L: the difference first, so that a
       // row whose every logit is the type's lowest value still has one.
-      const double m = static_cast<double>(w.m);
-      const double inv_l = 1.0 / static_cast<double>(w.l);
-      double lnL = log(static_cast<double>(w.l));
+      const double m = static_cast<double>(ref_max);
+      const double inv_l = 1.0 / sum_l;
+      double lnL = log(sum_l);
       // zs is off by zs_off of itself: d ln L / d ln zs = ln 2 E[arg]
-      if (is_policy(LOSS)) lnL -= a.zs_off * LN2 * static_cast<double>(w.t) * inv_l;
+      if (is_policy(LOSS)) lnL -= a.zs_off * LN2 * sum_t * inv_l;
       const float zy = L::load(&zy_raw);
       double total = 0.0;
-      RowCoef c{w.m, 0.f, 0.f, 0.f, 0.f};
+      RowCoef c{ref_max, 0.f, 0.f, 0.f, 0.f};
       if constexpr (is_policy(LOSS)) {
         const double lp = (static_cast<double>(zy == -INFINITY ? zy : lifted(zy)) - m) * a.inv_T - lnL;
-        const double H = lnL - static_cast<double>(w.t) * inv_l * LN2;
+        const double H = lnL - sum_t * inv_l * LN2;
         const PolicyRow r = policy_row(a.pol, pin, lp);
         total = r.loss;
         double a0 = -r.dlogp, a1 = 0.0;
@@ -841,10 +823,10 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
         if (a.kd != 0.0) total = a.kd * kl;
         double da = a.kd * Q * a.inv_T, db = 0.0;
         if (a.ce != 0.0) {
-          const double ln1 = LOSS == LOSS_DISTILL2 ? log(static_cast<double>(w.t)) : lnL;
+          const double ln1 = LOSS == LOSS_DISTILL2 ? log(sum_t) - EX2_BIAS : lnL;
           total += a.ce * (m - static_cast<double>(zy) + ln1);
           if constexpr (LOSS == LOSS_DISTILL2)
-            db = a.ce / static_cast<double>(w.t);
+            db = a.ce / sum_t;
           else
             da += a.ce;
         }
