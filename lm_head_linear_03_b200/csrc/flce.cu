@@ -927,7 +927,7 @@ LogitFit g_fit[MAX_FITS];
 int g_fits = 0;
 
 template <typename T, int LOSS, int THREADS>
-cudaError_t launch_logit_shape(const LogitArgs& a, int cs, int dev, size_t smem, cudaStream_t stream) {
+cudaError_t launch_logit_shape(const LogitArgs& a, int cs, int num_sms, int dev, size_t smem, cudaStream_t stream) {
   constexpr size_t RING = THREADS / 32 * WARP_RING_BYTES;
   const auto kernel = flce_logit_loss_kernel<T, LOSS, THREADS>;
   smem += RING;
@@ -942,7 +942,7 @@ cudaError_t launch_logit_shape(const LogitArgs& a, int cs, int dev, size_t smem,
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cs > 1 ? 1 : 0;
   int fit = 0;
   {
     const void* id = reinterpret_cast<const void*>(kernel);
@@ -954,8 +954,10 @@ cudaError_t launch_logit_shape(const LogitArgs& a, int cs, int dev, size_t smem,
       cudaError_t e;
       if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING + 32 * (DISTILL_MAX_K + 1))) !=
               cudaSuccess ||
-          (e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg)) != cudaSuccess)
+          (e = cs > 1 ? cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg)
+                      : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, THREADS, smem)) != cudaSuccess)
         return e;
+      if (cs == 1) fit *= num_sms;
       if (fit <= 0) return cudaErrorInvalidConfiguration;
       if (g_fits < MAX_FITS) g_fit[g_fits++] = {id, smem, dev, cs, fit};
     }
@@ -991,9 +993,9 @@ template <typename T, int LOSS>
 cudaError_t launch_logit_type(const LogitArgs& a, int num_sms, int dev, size_t smem, cudaStream_t stream) {
   const int cs = logit_cluster(a.N, a.V, sizeof(T), num_sms);
   switch (logit_threads(a.N, static_cast<int64_t>(a.V) * sizeof(T), cs, num_sms)) {
-    case 32: return launch_logit_shape<T, LOSS, 32>(a, cs, dev, smem, stream);
-    case LOGIT_THREADS / 2: return launch_logit_shape<T, LOSS, LOGIT_THREADS / 2>(a, cs, dev, smem, stream);
-    default: return launch_logit_shape<T, LOSS, LOGIT_THREADS>(a, cs, dev, smem, stream);
+    case 32: return launch_logit_shape<T, LOSS, 32>(a, cs, num_sms, dev, smem, stream);
+    case LOGIT_THREADS / 2: return launch_logit_shape<T, LOSS, LOGIT_THREADS / 2>(a, cs, num_sms, dev, smem, stream);
+    default: return launch_logit_shape<T, LOSS, LOGIT_THREADS>(a, cs, num_sms, dev, smem, stream);
   }
 }
 

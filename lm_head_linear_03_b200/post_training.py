@@ -15,7 +15,9 @@ not make ``stream`` wait for the streams that produced its inputs.
 from __future__ import annotations
 
 import torch
-from torch._C import _cuda_getCurrentRawStream as _current_stream_handle  # a few us less than current_stream()
+# the handles without the objects around them: a few us less per call
+from torch._C import _cuda_getCurrentRawStream as _current_stream_handle
+from torch._C import _cuda_getDevice as _current_device
 
 from .flce import REDUCTIONS, _check, _check_tensors, load_library
 
@@ -91,38 +93,34 @@ def _teacher(ids, logits, lse, N, dev):
     return K
 
 
-def _run(dev, stream, inputs, allocate, call):
-    """Runs ``call(outputs, stream handle)`` on ``dev``.  With a stream of the
-    caller's, outputs and scratch are allocated for that stream and the
-    allocator is told who else uses them and the inputs."""
+def _elsewhere(fn, dev, stream, args, kw):
+    """``fn(*args, **kw)`` on ``dev`` and, if given, ``stream``, neither of which
+    is current.  Outputs and scratch are allocated for that stream, and the
+    allocator is told who else uses the outputs and the inputs."""
     if stream is not None and stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return _run(dev, stream, inputs, allocate, call)
-    handle = _current_stream_handle(dev.index)
-    if stream is None or stream.cuda_stream == handle:
-        out = allocate()
-        call(out, handle)
-        return out
-    current = torch.cuda.current_stream()
-    with torch.cuda.stream(stream):
-        out = allocate()
-        call(out, stream.cuda_stream)
+    with torch.cuda.device(dev):
+        current = torch.cuda.current_stream()
+        if stream is None or stream == current:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kw)
     for t in out:
         if t is not None:
             t.record_stream(current)
-    for t in inputs:
-        if t is not None:
+    for t in (*args, *kw.values()):
+        if isinstance(t, torch.Tensor):
             t.record_stream(stream)
     return out
 
 
-def _workspace(ws, nbytes, dev):
+def _workspace(ws, nbytes, like):
+    """The caller's workspace, checked, or a new one on ``like``'s device."""
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if ws.dtype != torch.uint8 or ws.dim() != 1 or not ws.is_contiguous() or ws.device != dev or ws.numel() < nbytes:
-        raise ValueError(f"workspace must be a contiguous 1-D uint8 tensor of at least {nbytes} bytes on {dev}")
+        return like.new_empty(nbytes, dtype=torch.uint8)
+    if (ws.dtype != torch.uint8 or ws.dim() != 1 or not ws.is_contiguous() or ws.device != like.device
+            or ws.numel() < nbytes):
+        raise ValueError(f"workspace must be a contiguous 1-D uint8 tensor of at least {nbytes} bytes on {like.device}")
     return ws
 
 
@@ -145,21 +143,21 @@ def clipped_policy(row_loss, y, old_logp, advantages, *, ref_logp=None, clip_low
     _vec(advantages, torch.float32, N, dev, "advantages")
     _vec(ref_logp, torch.float32, N, dev, "ref_logp", optional=True)
     red = _scale(row_scale, reduction, N, dev, "row_scale")
+    if stream is not None or dev.index != _current_device():
+        return _elsewhere(clipped_policy, dev, stream, (row_loss, y, old_logp, advantages),
+                          dict(ref_logp=ref_logp, clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef,
+                               reduction=reduction, row_scale=row_scale, ignore_index=ignore_index,
+                               workspace=workspace))
     nbytes = lib.flce_ce_workspace_size(N, 1) if N > CLIPPED_POLICY_NO_WORKSPACE else 0
-
-    def allocate():
-        return (torch.empty(1, dtype=torch.float64, device=dev), torch.empty(N, dtype=torch.float32, device=dev),
-                torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev),
-                torch.empty(1, dtype=torch.int32, device=dev), _workspace(workspace, nbytes, dev) if nbytes else None)
-
-    def call(o, s):
-        loss, rows, kl, weight, status, ws = o
-        _check(lib.flce_clipped_policy(_p(row_loss), _p(y), N, ignore_index, _p(old_logp), _p(advantages),
-                                       _p(ref_logp), clip_low, clip_high, kl_coef, red, _p(row_scale), _p(loss),
-                                       _p(rows), _p(kl), _p(weight), _p(status), _p(ws), nbytes, s),
-               "flce_clipped_policy")
-
-    return _run(dev, stream, (row_loss, y, old_logp, advantages, ref_logp, row_scale), allocate, call)[:5]
+    ws = _workspace(workspace, nbytes, row_loss) if nbytes else None
+    loss = row_loss.new_empty(1, dtype=torch.float64)
+    rows, kl, weight = row_loss.new_empty(N), row_loss.new_empty(N), row_loss.new_empty(N)
+    status = y.new_empty(1)
+    _check(lib.flce_clipped_policy(_p(row_loss), _p(y), N, ignore_index, _p(old_logp), _p(advantages), _p(ref_logp),
+                                   clip_low, clip_high, kl_coef, red, _p(row_scale), _p(loss), _p(rows), _p(kl),
+                                   _p(weight), _p(status), _p(ws), nbytes, _current_stream_handle(dev.index)),
+           "flce_clipped_policy")
+    return loss, rows, kl, weight, status
 
 
 def policy_loss(logits, y, old_logp, advantages, *, ref_logp=None, clip_low: float = 0.2, clip_high: float = 0.2,
@@ -177,24 +175,23 @@ def policy_loss(logits, y, old_logp, advantages, *, ref_logp=None, clip_low: flo
     _vec(advantages, torch.float32, N, dev, "advantages")
     _vec(ref_logp, torch.float32, N, dev, "ref_logp", optional=True)
     red = _scale(grad_row_scale, reduction, N, dev, "grad_row_scale")
-    nbytes = lib.flce_ce_workspace_size(N, V)
-    ldg = ld
-
-    def allocate():
-        nonlocal ldg
-        g, ldg = _grad_like(logits, ld, grad)
-        return (torch.empty(1, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev),
-                torch.empty(N, dtype=torch.float32, device=dev), torch.empty(N, dtype=torch.float32, device=dev),
-                torch.empty(N, dtype=torch.float32, device=dev), g, _workspace(workspace, nbytes, dev))
-
-    def call(o, s):
-        loss, status, logp, entropy, kl, g, ws = o
-        _check(lib.flce_policy_loss(_p(logits), DTYPES[logits.dtype], ld, _p(y), N, V, ignore_index, temperature,
-                                    _p(old_logp), _p(advantages), _p(ref_logp), clip_low, clip_high, kl_coef,
-                                    entropy_coef, red, _p(grad_row_scale), _p(loss), _p(logp), _p(entropy), _p(kl),
-                                    _p(status), _p(g), ldg, _p(ws), ws.numel(), s), "flce_policy_loss")
-
-    return _run(dev, stream, (logits, y, old_logp, advantages, ref_logp, grad_row_scale), allocate, call)[:6]
+    if stream is not None or dev.index != _current_device():
+        return _elsewhere(policy_loss, dev, stream, (logits, y, old_logp, advantages),
+                          dict(ref_logp=ref_logp, clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef,
+                               entropy_coef=entropy_coef, temperature=temperature, reduction=reduction,
+                               grad_row_scale=grad_row_scale, ignore_index=ignore_index, grad=grad,
+                               workspace=workspace))
+    ws = _workspace(workspace, lib.flce_ce_workspace_size(N, V), y)
+    g, ldg = _grad_like(logits, ld, grad)
+    loss, logp, entropy, kl = (advantages.new_empty(1), advantages.new_empty(N), advantages.new_empty(N),
+                               advantages.new_empty(N))
+    status = y.new_empty(1)
+    _check(lib.flce_policy_loss(_p(logits), DTYPES[logits.dtype], ld, _p(y), N, V, ignore_index, temperature,
+                                _p(old_logp), _p(advantages), _p(ref_logp), clip_low, clip_high, kl_coef,
+                                entropy_coef, red, _p(grad_row_scale), _p(loss), _p(logp), _p(entropy), _p(kl),
+                                _p(status), _p(g), ldg, _p(ws), ws.numel(), _current_stream_handle(dev.index)),
+           "flce_policy_loss")
+    return loss, status, logp, entropy, kl, g
 
 
 def distill_topk(logits, y, teacher_ids, teacher_logits, *, teacher_lse=None, temperature: float = 1.0,
@@ -210,25 +207,22 @@ def distill_topk(logits, y, teacher_ids, teacher_logits, *, teacher_lse=None, te
     dev = logits.device
     K = _teacher(teacher_ids, teacher_logits, teacher_lse, N, dev)
     red = _scale(grad_row_scale, reduction, N, dev, "grad_row_scale")
-    nbytes = lib.flce_ce_workspace_size(N, V)
-    ldg = ld
-
-    def allocate():
-        nonlocal ldg
-        g, ldg = _grad_like(logits, ld, grad)
-        return (torch.empty(1, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev),
-                torch.empty(N, dtype=torch.float32, device=dev) if row_loss else None, g,
-                _workspace(workspace, nbytes, dev))
-
-    def call(o, s):
-        loss, status, rows, g, ws = o
-        _check(lib.flce_distill_topk(_p(logits), DTYPES[logits.dtype], ld, _p(y), N, V, ignore_index,
-                                     _p(teacher_ids), _p(teacher_logits), DTYPES[teacher_logits.dtype], K,
-                                     _p(teacher_lse), temperature, kd_weight, ce_weight, red, _p(grad_row_scale),
-                                     _p(loss), _p(rows), _p(status), _p(g), ldg, _p(ws), ws.numel(), s),
-               "flce_distill_topk")
-
-    return _run(dev, stream, (logits, y, teacher_ids, teacher_logits, teacher_lse, grad_row_scale), allocate, call)[:4]
+    if stream is not None or dev.index != _current_device():
+        return _elsewhere(distill_topk, dev, stream, (logits, y, teacher_ids, teacher_logits),
+                          dict(teacher_lse=teacher_lse, temperature=temperature, kd_weight=kd_weight,
+                               ce_weight=ce_weight, reduction=reduction, grad_row_scale=grad_row_scale,
+                               ignore_index=ignore_index, row_loss=row_loss, grad=grad, workspace=workspace))
+    ws = _workspace(workspace, lib.flce_ce_workspace_size(N, V), y)
+    g, ldg = _grad_like(logits, ld, grad)
+    loss = y.new_empty(1, dtype=torch.float32)
+    rows = y.new_empty(N, dtype=torch.float32) if row_loss else None
+    status = y.new_empty(1)
+    _check(lib.flce_distill_topk(_p(logits), DTYPES[logits.dtype], ld, _p(y), N, V, ignore_index, _p(teacher_ids),
+                                 _p(teacher_logits), DTYPES[teacher_logits.dtype], K, _p(teacher_lse), temperature,
+                                 kd_weight, ce_weight, red, _p(grad_row_scale), _p(loss), _p(rows), _p(status),
+                                 _p(g), ldg, _p(ws), ws.numel(), _current_stream_handle(dev.index)),
+           "flce_distill_topk")
+    return loss, status, rows, g
 
 
 def _head_outputs(X, W, grads):
@@ -260,21 +254,21 @@ def policy_forward_backward(X, W, y, old_logp, advantages, *, ref_logp=None, cli
     _vec(mean_count, torch.int32, 1, dev, "mean_count", optional=True)
     red = _scale(grad_row_scale, reduction, N, dev, "grad_row_scale")
 
-    def allocate():
-        return (torch.empty(1, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev),
-                torch.empty(N, dtype=torch.float32, device=dev), *_head_outputs(X, W, grads),
-                torch.empty(policy_workspace_size(N, H, V), dtype=torch.uint8, device=dev)
-                if workspace is None else workspace)
-
-    def call(o, s):
-        loss, status, logp, dX, dW, ws = o
-        _check(lib.flce_policy_forward_backward(_p(X), _p(W), _p(y), N, H, V, ignore_index, _p(old_logp),
-                                                _p(advantages), _p(ref_logp), clip_low, clip_high, kl_coef, red,
-                                                _p(grad_row_scale), _p(mean_count), _p(loss), _p(logp), _p(status),
-                                                _p(dX), _p(dW), _p(ws), ws.numel(), s),
-               "flce_policy_forward_backward")
-
-    return _run(dev, stream, (X, W, y, old_logp, advantages, ref_logp, grad_row_scale, mean_count), allocate, call)[:5]
+    if stream is not None or dev.index != _current_device():
+        return _elsewhere(policy_forward_backward, dev, stream, (X, W, y, old_logp, advantages),
+                          dict(ref_logp=ref_logp, clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef,
+                               reduction=reduction, grad_row_scale=grad_row_scale, mean_count=mean_count,
+                               ignore_index=ignore_index, grads=grads, workspace=workspace))
+    ws = y.new_empty(policy_workspace_size(N, H, V), dtype=torch.uint8) if workspace is None else workspace
+    loss, logp = advantages.new_empty(1), advantages.new_empty(N)
+    status = y.new_empty(1)
+    dX, dW = _head_outputs(X, W, grads)
+    _check(lib.flce_policy_forward_backward(_p(X), _p(W), _p(y), N, H, V, ignore_index, _p(old_logp), _p(advantages),
+                                            _p(ref_logp), clip_low, clip_high, kl_coef, red, _p(grad_row_scale),
+                                            _p(mean_count), _p(loss), _p(logp), _p(status), _p(dX), _p(dW), _p(ws),
+                                            ws.numel(), _current_stream_handle(dev.index)),
+           "flce_policy_forward_backward")
+    return loss, status, logp, dX, dW
 
 
 def distill_workspace_size(N: int, H: int, V: int, K: int, reorder: bool = False) -> int:
@@ -300,19 +294,21 @@ def distill_forward_backward(X, W, y, teacher_ids, teacher_logits, *, teacher_ls
     _vec(mean_count, torch.int32, 1, dev, "mean_count", optional=True)
     red = _scale(grad_row_scale, reduction, N, dev, "grad_row_scale")
 
-    def allocate():
-        return (torch.empty(1, dtype=torch.float32, device=dev), torch.empty(1, dtype=torch.int32, device=dev),
-                torch.empty(N, dtype=torch.float32, device=dev) if row_loss else None, *_head_outputs(X, W, grads),
-                torch.empty(distill_workspace_size(N, H, V, K), dtype=torch.uint8, device=dev)
-                if workspace is None else workspace)
-
-    def call(o, s):
-        loss, status, rows, dX, dW, ws = o
-        _check(lib.flce_distill_forward_backward(_p(X), _p(W), _p(y), N, H, V, ignore_index, _p(teacher_ids),
-                                                 _p(teacher_logits), DTYPES[teacher_logits.dtype], K, _p(teacher_lse),
-                                                 temperature, kd_weight, ce_weight, red, _p(grad_row_scale),
-                                                 _p(mean_count), _p(loss), _p(rows), _p(status), _p(dX), _p(dW),
-                                                 _p(ws), ws.numel(), s), "flce_distill_forward_backward")
-
-    return _run(dev, stream, (X, W, y, teacher_ids, teacher_logits, teacher_lse, grad_row_scale, mean_count),
-                allocate, call)[:5]
+    if stream is not None or dev.index != _current_device():
+        return _elsewhere(distill_forward_backward, dev, stream, (X, W, y, teacher_ids, teacher_logits),
+                          dict(teacher_lse=teacher_lse, temperature=temperature, kd_weight=kd_weight,
+                               ce_weight=ce_weight, reduction=reduction, grad_row_scale=grad_row_scale,
+                               mean_count=mean_count, ignore_index=ignore_index, row_loss=row_loss, grads=grads,
+                               workspace=workspace))
+    ws = y.new_empty(distill_workspace_size(N, H, V, K), dtype=torch.uint8) if workspace is None else workspace
+    loss = y.new_empty(1, dtype=torch.float32)
+    rows = y.new_empty(N, dtype=torch.float32) if row_loss else None
+    status = y.new_empty(1)
+    dX, dW = _head_outputs(X, W, grads)
+    _check(lib.flce_distill_forward_backward(_p(X), _p(W), _p(y), N, H, V, ignore_index, _p(teacher_ids),
+                                             _p(teacher_logits), DTYPES[teacher_logits.dtype], K, _p(teacher_lse),
+                                             temperature, kd_weight, ce_weight, red, _p(grad_row_scale),
+                                             _p(mean_count), _p(loss), _p(rows), _p(status), _p(dX), _p(dW), _p(ws),
+                                             ws.numel(), _current_stream_handle(dev.index)),
+           "flce_distill_forward_backward")
+    return loss, status, rows, dX, dW
