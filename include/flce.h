@@ -353,10 +353,11 @@ flce_status_t flce_clipped_policy(const float* d_row_loss, const int32_t* y, int
 /* The same loss on given logits z, with an entropy term.  With x = z / temperature,
  *   lp_i = x_{i,y_i} - lse(x_i),  H_i = -sum_j p_ij log p_ij,
  *   L_i as above - entropy_coef H_i;
- * dlogits = d loss / d z (temperature's 1/T included).  d_logp, d_entropy and
+ * dlogits = d loss / d z (temperature's 1/T included); temperature in
+ * [1e-6, 1e6].  d_logp, d_entropy and
  * d_kl (DEVICE fp32 [N]) receive lp, H and kl, 0 on ignored rows.  A logit of
  * -infinity is a vocabulary entry of probability 0; lower finite logits than
- * -2^100 count as -2^100.  Targets outside [0, V) set
+ * -2^40 count as -2^40.  Targets outside [0, V) set
  * FLCE_ERR_TARGET_OUT_OF_RANGE in d_status and count as ignored in the sums.
  * workspace: flce_ce_workspace_size(N, V) bytes.  Asynchronous; may be
  * captured in a CUDA graph. */

@@ -836,6 +836,10 @@ flce_status_t check_reduction(int32_t r) {
 
 bool is_finite(double x) { return x - x == 0.0; }
 
+// Within this range no product of a logit's difference with 1 / T leaves fp32
+// where the logits are at least -2^40, which the policy loss raises them to.
+bool temperature_ok(double t) { return t >= 1e-6 && t <= 1e6; }
+
 // The policy loss's clip widths and KL weight.
 flce_status_t check_policy(double clip_low, double clip_high, double kl_coef, const float* d_ref_logp) {
   if (!(clip_low >= 0.0 && clip_low <= 1.0) || !(clip_high >= 0.0) || !is_finite(kl_coef)) return FLCE_ERR_INVALID_ARGUMENT;
@@ -862,7 +866,7 @@ size_t dtype_bytes(int32_t dtype) {
 flce_status_t check_teacher(const int32_t* ids, const void* logits, int32_t dtype, int32_t K, const float* lse,
                             double temperature, double kd, double ce) {
   if (!ids || !logits || K <= 0 || K > DISTILL_MAX_K || dtype_bytes(dtype) == 0) return FLCE_ERR_INVALID_ARGUMENT;
-  if (!(temperature > 0.0) || !is_finite(temperature) || !is_finite(1.0 / temperature) || !is_finite(kd) || !is_finite(ce))
+  if (!temperature_ok(temperature) || !is_finite(kd) || !is_finite(ce))
     return FLCE_ERR_INVALID_ARGUMENT;
   if (!aligned(ids, 4) || !aligned(logits, dtype_bytes(dtype)) || !aligned(lse, 4)) return FLCE_ERR_UNSUPPORTED;
   return FLCE_OK;
@@ -1303,7 +1307,7 @@ flce_status_t flce_policy_loss(const void* logits, int32_t dtype, int64_t ld, co
   if (s != FLCE_OK) return s;
   if (!y || !d_advantage || !d_loss || !d_logp || !d_entropy || !d_kl || !d_status || !workspace)
     return FLCE_ERR_INVALID_ARGUMENT;
-  if (!(temperature > 0.0) || !is_finite(temperature) || !is_finite(1.0 / temperature) || !is_finite(entropy_coef))
+  if (!temperature_ok(temperature) || !is_finite(entropy_coef))
     return FLCE_ERR_INVALID_ARGUMENT;
   for (const void* p : {static_cast<const void*>(y), static_cast<const void*>(d_old_logp),
                         static_cast<const void*>(d_advantage), static_cast<const void*>(d_ref_logp),

@@ -35,7 +35,7 @@ constexpr int DISTILL_MAX_K = 1024;
 // the difference stays finite, so that a probability of 0 adds 0.  A register
 // without a logit holds LOGIT_NONE, which has probability 0 beside any logit.
 // Powers of two: the same value in bf16.
-constexpr float LOGIT_LOWEST = -0x1p100f, LOGIT_NONE = -0x1p102f;
+constexpr float LOGIT_LOWEST = -0x1p40f, LOGIT_NONE = -0x1p42f;
 constexpr float NEG_BIG = -1e4f;  // exponents below this are 0 in every format; finite, so that 0 * it is 0
 
 // ------------------------------------------------------- logits by type --
@@ -388,9 +388,6 @@ struct RowStat {
 // How far a logit may lie above the reference, in the exponent, before the
 // reference moves: rarely, because each move rounds the sums.
 constexpr float RAISE = 60.f;
-// Mean relative error of the hardware's 2^x over arguments below -1, measured:
-// it does not average out of a sum of exponentials.
-constexpr double EX2_BIAS = -5.0e-8;
 
 // What the gradient needs of a row.
 struct RowCoef {
@@ -627,18 +624,18 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
     }
     auto read_entries = [&]() {
       if constexpr (!is_policy(LOSS)) {
-      for (int k = tid; k < K1; k += THREADS) {
-        const int id = checked(k == tid ? my_id : teacher_id(k));
-        const float u = k == tid ? my_u : teacher_u(k);
-        s_id[k] = id;
-        s_u[k] = id < 0 ? -INFINITY : u;
-        if (k == tid) {
-          my_id = id;
-          if (wanted(id)) my_z = p.z[id];
-        } else {
-          s_z[k] = wanted(id) ? L::load(p.z + id) : 0.f;
+        for (int k = tid; k < K1; k += THREADS) {
+          const int id = checked(k == tid ? my_id : teacher_id(k));
+          const float u = k == tid ? my_u : teacher_u(k);
+          s_id[k] = id;
+          s_u[k] = id < 0 ? -INFINITY : u;
+          if (k == tid) {
+            my_id = id;
+            if (wanted(id)) my_z = p.z[id];
+          } else {
+            s_z[k] = wanted(id) ? L::load(p.z + id) : 0.f;
+          }
         }
-      }
       }
     };
 
@@ -771,7 +768,6 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
         sum_l += __shfl_xor_sync(0xffffffffu, sum_l, s);
         sum_t += __shfl_xor_sync(0xffffffffu, sum_t, s);
       }
-      sum_l *= 1.0 - EX2_BIAS;
       if (is_policy(LOSS) && !__any_sync(0xffffffffu, top > 0.f)) sum_l = 0.0;  // every logit is -infinity: NaN
       // Log-probabilities as (z - m)/T - ln L: the difference first, so that a
       // row whose every logit is the type's lowest value still has one.
@@ -823,7 +819,7 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
         if (a.kd != 0.0) total = a.kd * kl;
         double da = a.kd * Q * a.inv_T, db = 0.0;
         if (a.ce != 0.0) {
-          const double ln1 = LOSS == LOSS_DISTILL2 ? log(sum_t) - EX2_BIAS : lnL;
+          const double ln1 = LOSS == LOSS_DISTILL2 ? log(sum_t) : lnL;
           total += a.ce * (m - static_cast<double>(zy) + ln1);
           if constexpr (LOSS == LOSS_DISTILL2)
             db = a.ce / sum_t;
@@ -891,19 +887,19 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
         uint4* tile = ring + stage * TILE_CHUNKS;
         auto write_tile = [&](auto full) {
 #pragma unroll
-        for (int u = 0; u < LANE_CHUNKS; ++u) {
-          if (decltype(full)::value || u * 32 + lane < size) {
-            uint4 v = tile[u * 32 + lane], o;
-            if constexpr (is_policy(LOSS)) L::clamp(v);
+          for (int u = 0; u < LANE_CHUNKS; ++u) {
+            if (decltype(full)::value || u * 32 + lane < size) {
+              uint4 v = tile[u * 32 + lane], o;
+              if constexpr (is_policy(LOSS)) L::clamp(v);
 #pragma unroll
-            for (int i = 0; i < EPC / 2; ++i) {
-              float lo, hi;
-              f32x2_split(dense2(L::pair(v, i)), lo, hi);
-              L::put(o, i, lo, hi);
+              for (int i = 0; i < EPC / 2; ++i) {
+                float lo, hi;
+                f32x2_split(dense2(L::pair(v, i)), lo, hi);
+                L::put(o, i, lo, hi);
+              }
+              tile[u * 32 + lane] = o;
             }
-            tile[u * 32 + lane] = o;
           }
-        }
         };
         if (size == TILE_CHUNKS)
           write_tile(Flag<true>{});

@@ -181,7 +181,7 @@ def _policy(lib, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(z=None, dz=None), 1), (dict(dt=3), 1), (dict(ld=59, ldg=59), 1), (dict(ldg=59), 1), (dict(ldg=65), 1),
     (dict(dz=FAKE + 2), 1), (dict(dz=FAKE + (7 * 64 + 60) * 2 - 2), 1), (dict(V=0), 1), (dict(T=0.0), 1), (dict(T=-1.0), 1),
-    (dict(T=NAN), 1), (dict(T=INF), 1), (dict(T=1e-320), 1), (dict(ent=NAN), 1), (dict(logp=None), 1), (dict(H=None), 1),
+    (dict(T=NAN), 1), (dict(T=INF), 1), (dict(T=1e-7), 1), (dict(T=2e6), 1), (dict(ent=NAN), 1), (dict(logp=None), 1), (dict(H=None), 1),
     (dict(z=FAKE + 1, dz=FAKE + 1), 2), (dict(status=FAKE + 2), 2), (dict(nbytes=100), 3)])
 def test_policy_loss_refusals(lib, kw, status):
     assert _policy(lib, **kw) == status

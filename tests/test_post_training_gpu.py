@@ -181,6 +181,37 @@ def test_policy_masked_vocabulary(dtype, low):
     _check_policy(Z, y, old, adv, ref, kl=0.05, ent=0.03)
 
 
+@pytest.mark.parametrize("T", [1e-6, 1e-3, 1e3, 1e6])
+@pytest.mark.parametrize("dtype", DT, ids=["bf16", "fp16", "fp32"])
+def test_temperature_range(T, dtype):
+    """The ends of the range, with masked entries, beside the same softmax of
+    pre-scaled logits at temperature 1 (logits of T's magnitude, powers of two
+    apart, so that both are the same numbers)."""
+    F = _lib()
+    g = torch.Generator().manual_seed(3)
+    step = 2.0 ** round(math.log2(T))
+    Z = torch.randint(-6, 7, (9, 300), generator=g).double() * step
+    Z = Z.clamp(-60000, 60000) if dtype is torch.float16 else Z
+    if dtype is torch.float16 and T < 1e-3:
+        pytest.skip("logits of this size are not fp16 numbers")
+    Z = Z.to(dtype)
+    mask = torch.rand(9, 300, generator=g) < 0.3
+    mask[:, 0] = False
+    Z = Z.masked_fill(mask, -math.inf)
+    y = torch.zeros(9, dtype=torch.int32)
+    adv = torch.randn(9, generator=g)
+    out = F.policy_loss(*_cuda(Z, y), None, adv.cuda(), temperature=T, entropy_coef=0.1)
+    ref = O.policy_reference(Z, y, None, adv, None, entropy_coef=0.1, temperature=T)
+    assert torch.isfinite(out[5]).all()
+    _close(_np(out[2]), ref[2], 1e-5 * (1 + np.abs(ref[2])), "logp")
+    _close(_np(out[3]), ref[3], 1e-5 * (1 + np.abs(ref[3])), "entropy")
+    ids, u = teacher_case(9, 300, 5)
+    ids = torch.where(mask.gather(1, ids.long().clamp(min=0)), -1, ids).to(torch.int32)
+    _, _, rows, gd = F.distill_topk(*_cuda(Z, y, ids, u * step), temperature=T, row_loss=True)
+    want = O.distill_reference(Z, y, ids, u * step, temperature=T)
+    _close(_np(rows), want[2], 1e-5 * (1 + np.abs(want[2])), "row loss")
+
+
 def test_policy_bad_values_stay_in_their_rows():
     F = _lib()
     Z, y, old, adv, ref = policy_case(8, 300, seed=10, ign=0.0)
