@@ -131,6 +131,62 @@ def test_policy_options(kl, ent, T, reduction, dtype):
     _check_policy(Z, y, old, adv, ref if kl else None, kl=kl, ent=ent, T=T, reduction=reduction, scale=scale)
 
 
+# More rows than run at the same time, in each shape of CTA (one warp, four,
+# eight, clusters), with rows of every alignment, long and scattered gaps.
+MANY = [(2600, 1001), (700, 20003), (330, 60001), (160, 140001)]
+
+
+def _gaps(y):
+    y = y.clone()
+    n = len(y)
+    y[n // 8: n // 3] = IGN
+    y[-3:] = IGN
+    return y
+
+
+@pytest.mark.parametrize("N,V", MANY)
+@pytest.mark.parametrize("grad", ["new", "inplace"])
+def test_policy_many_rows(N, V, grad):
+    Z, y, old, adv, ref = policy_case(N, V, seed=N, dtype=torch.bfloat16, ign=0.25)
+    _check_policy(Z, _gaps(y), old, adv, ref, ent=0.01 if grad == "new" else 0.0, grad=grad)
+
+
+@pytest.mark.parametrize("N,V", MANY)
+def test_distill_many_rows(N, V):
+    Z, y, *_ = policy_case(N, V, seed=N, dtype=torch.float16, ign=0.25)
+    g = torch.Generator().manual_seed(N)
+    ids = torch.randint(0, V, (N, 40), generator=g, dtype=torch.int64).to(torch.int32)
+    ids[:, 30:] = ids[:, :10] // 2                 # clustered, some of them twice
+    u = torch.randn(N, 40, generator=g) * 2
+    _check_distill(Z, _gaps(y), ids, u, ce=0.25)
+
+
+def test_rows_behind_two_to_the_31_elements():
+    """17000 x 128256 logits: the last rows lie beyond 2^31 elements."""
+    F = _lib()
+    N, V = 17000, 128256
+    g = torch.Generator(device="cuda").manual_seed(5)
+    Z = torch.empty(N, V, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, N, 1000):
+        Z[i:i + 1000] = torch.randn(1000, V, generator=g, device="cuda")
+    y = torch.randint(0, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    adv = torch.randn(N, generator=g, device="cuda")
+    y[: N - 40] = IGN
+    pick = torch.arange(N - 40, N, device="cuda")
+    want = O.policy_reference(Z[pick].cpu(), y[pick].cpu(), None, adv[pick].cpu())
+    loss, status, lp, H, kl, dz = F.policy_loss(Z, y, None, adv)
+    assert status.item() == 0
+    _close(_np(lp[pick]), want[2], _delta(V) + np.abs(want[2]) * EPS32, "logp")
+    assert_grad_close(_np(dz[pick]), want[1], "dlogits")
+    assert not any(torch.count_nonzero(dz[i:i + 1000]).item() for i in range(0, N - 1000, 1000))
+    ids = torch.randint(0, V, (N, 20), generator=g, device="cuda", dtype=torch.int32)
+    u = torch.randn(N, 20, generator=g, device="cuda")
+    want = O.distill_reference(Z[pick].cpu(), y[pick].cpu(), ids[pick].cpu(), u[pick].cpu())
+    loss, status, rows, _ = F.distill_topk(Z, y, ids, u, row_loss=True, grad="inplace")
+    _close(_np(rows[pick]), want[2], 1e-5 * (1 + np.abs(want[2])), "row loss")
+    assert_grad_close(_np(Z[pick]), want[1], "dlogits in place")
+
+
 def test_policy_on_policy_and_metrics_only():
     Z, y, old, adv, ref = policy_case(33, 515, seed=6)
     _check_policy(Z, y, None, adv, ref, kl=0.1)       # ratio 1
