@@ -161,6 +161,37 @@ def test_distill_many_rows(N, V):
     _check_distill(Z, _gaps(y), ids, u, ce=0.25)
 
 
+@pytest.mark.parametrize("which", ["every_third", "last", "first_half", "none"])
+def test_policy_rows_that_do_not_count(which):
+    """Long rows, more of them than run at the same time: wherever those lie that
+    count, they have their results and the others zeros; targets outside [0, V)
+    are reported and counted, and nothing behind a row's V entries is written."""
+    F = _lib()
+    N, V, pad = 900, 52001, 3
+    g = torch.Generator().manual_seed(9)
+    Z = torch.randn(N, V, generator=g).bfloat16()
+    y = torch.randint(0, V, (N,), generator=g, dtype=torch.int64).to(torch.int32)
+    adv = torch.randn(N, generator=g)
+    i = torch.arange(N)
+    keep = {"every_third": i % 3 == 1, "last": i == N - 1, "first_half": i < N // 2, "none": i < 0}[which]
+    y[~keep] = IGN
+    y[N - 2], y[5] = V, -7
+    pick = torch.nonzero(keep & (y >= 0) & (y < V)).flatten().tolist()
+    Zd, buf = _padded(Z, pad)
+    loss, status, lp, H, kl, dz = F.policy_loss(Zd, y.cuda(), None, adv.cuda(), entropy_coef=0.01, grad="inplace")
+    assert status.item() == 4
+    assert dz.data_ptr() == Zd.data_ptr() and torch.isnan(buf[:, V:]).all()
+    off = torch.ones(N, dtype=torch.bool)
+    off[pick] = False
+    for t in (lp, H, kl, dz):
+        assert torch.count_nonzero(t[off.cuda()]).item() == 0
+    if len(pick):
+        want = O.policy_reference(Z[pick], y[pick], None, adv[pick], entropy_coef=0.01)
+        _close(_np(lp)[pick], want[2], _delta(V) + np.abs(want[2]) * EPS32, "logp")
+        count = int((y != IGN).sum())  # the mean is over all rows that are not ignored
+        assert_grad_close(_np(dz)[pick], want[1] * (len(pick) / count), "dlogits")
+
+
 def test_rows_behind_two_to_the_31_elements():
     """17000 x 128256 logits: the last rows lie beyond 2^31 elements."""
     F = _lib()
