@@ -644,8 +644,10 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
     if (is_policy(LOSS)) edge = edge_col >= 0 ? lifted(edge) : none;
     float ref = is_policy(LOSS) ? LOGIT_LOWEST : -FLT_MAX;  // the warp's reference
     uint64_t l2 = 0ull, t2 = 0ull;                          // this lane's sums, in two parts each
+    // in the exponents of the sharper softmax, where there are two
+    const float steep = LOSS == LOSS_DISTILL2 ? fmaxf(a.zs, LOG2E) : a.zs;
     auto raise = [&](float lane_top) {  // the reference, where some lane's logits need it
-      if (!__any_sync(0xffffffffu, (lane_top - ref) * a.zs > RAISE)) return;
+      if (!__any_sync(0xffffffffu, (lane_top - ref) * steep > RAISE)) return;
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) lane_top = fmaxf(lane_top, __shfl_xor_sync(0xffffffffu, lane_top, s));
       const float d = (ref - lane_top) * a.zs, f = ex2_approx(d);

@@ -432,6 +432,22 @@ def test_distill_options(T, kd, ce, reduction, dtype, given):
     _check_distill(Z, y, ids, u, lse=lse, T=T, kd=kd, ce=ce, reduction=reduction, scale=scale)
 
 
+@pytest.mark.parametrize("dtype", DT, ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T,gap", [(3.0, 110.0), (50.0, 1000.0), (1000.0, 20000.0)])
+def test_distill_peak_behind_the_first_tiles(T, gap, dtype):
+    """A logit `gap` above the others, behind a warp's first tile: near them at
+    temperature T, beyond fp32's exponents (88) at that of the hard labels."""
+    N, V, K = 6, 200001, 9
+    g = torch.Generator().manual_seed(12)
+    Z = torch.randn(N, V, generator=g)
+    at = torch.tensor([17000, 43000, 69500, 95001, 120002, V - 1])
+    Z[torch.arange(N), at] += gap
+    ids, u = teacher_case(N, V, K, seed=3)
+    y = torch.randint(0, V, (N,), generator=g, dtype=torch.int64).to(torch.int32)
+    y[::2] = at[::2].to(torch.int32)
+    _check_distill(Z.to(dtype), y, ids, u, T=T, ce=0.5)
+
+
 def test_distill_same_id_twice_and_target_in_the_list():
     Z, y, *_ = policy_case(30, 60, seed=13)
     ids, u = teacher_case(30, 60, 48, seed=14, duplicates=True)
