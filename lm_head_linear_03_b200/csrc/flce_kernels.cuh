@@ -314,7 +314,9 @@ __device__ __forceinline__ void epi_lse_tile(const GemmArgs& a, uint32_t taddr, 
   }
 }
 
-// One vocabulary range's share of dX, added up over the chunks in fp32.  Each
+// One vocabulary range's share of dX, added up over the chunks in fp32: a head
+// of few rows has fewer dX tiles than there are SM pairs, each with the whole
+// vocabulary to go through (256 x 256 has one; the call takes 51 us with ranges).  Each
 // thread holds a row: 128 contiguous bytes of it per slice, whole sectors.  The
 // sum of the chunk before was written by another SM, behind the counter this
 // item has waited for: it is read past L1.
@@ -1687,7 +1689,8 @@ __global__ void __launch_bounds__(256)
 
 // Joins the vocabulary ranges' shares of dX (KS > 1): their sum in range order,
 // rounded once, in the caller's row order; rows of all-ignored tiles, which no
-// item computed, are zero.  A thread takes eight columns.
+// item computed, are zero.  A thread takes eight columns.  Bound by reading the
+// shares: 2048 x 2304 in three ranges (57 MB) 13 us, 256 x 256 in 4 to 5 us.
 __global__ void __launch_bounds__(256)
     flce_dx_join_kernel(const float* part, int KS, uint16_t* dX, const int* perm, const int* tile_valid, int N, int H) {
   const int h8 = H / 8;
