@@ -246,7 +246,7 @@ struct PolicyRowsArgs {
 // Elementwise over the rows, with two fp64 exponentials (the ratio, the KL term) in
 // each.  A thread takes four neighbouring rows, so that the loads of each of its up
 // to six streams are one 16-byte access where the stream allows it.  Measured, both
-// launches in a graph: 1,048,576 rows (29 MB) 16.4 us, 4,194,304 rows 43 us, 2.7 TB/s.
+// launches in a graph: 1,048,576 rows (34 MB) 16.4 us, 4,194,304 rows 43 us, 3.1 TB/s.
 // Instructions of the fp64 functions bound it (52% of the issue slots, the fp64
 // pipe 23%); fewer registers for 5, 6 or 8 CTAs on an SM: 44.0, 45.3, 46.5 us.
 constexpr int POLICY_THREADS = 256;
