@@ -1690,7 +1690,7 @@ __global__ void __launch_bounds__(256)
 // Joins the vocabulary ranges' shares of dX (KS > 1): their sum in range order,
 // rounded once, in the caller's row order; rows of all-ignored tiles, which no
 // item computed, are zero.  A thread takes eight columns.  Bound by reading the
-// shares: 2048 x 2304 in three ranges (57 MB) 13 us, 256 x 256 in 4 to 5 us.
+// shares: three ranges of 2048 x 2304 (57 MB) 13 us, those of 256 x 256 4 to 5 us.
 __global__ void __launch_bounds__(256)
     flce_dx_join_kernel(const float* part, int KS, uint16_t* dX, const int* perm, const int* tile_valid, int N, int H) {
   const int h8 = H / 8;
