@@ -514,6 +514,7 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
   if (tid == 0) abort_flag = 0;
   fence_mbar_init();
   __syncthreads();
+  if (cs > 1) cluster_sync_all();  // the others run before a record is written into their shared memory
   const int n_valid = count_rows(a.valid);
   const double inv_n = n_valid > 0 ? 1.0 / static_cast<double>(n_valid) : 0.0;
   const int walks = a.g ? 2 : 1;
