@@ -315,7 +315,9 @@ flce_status_t flce_pairwise_logistic(const float* d_row_loss, const int32_t* y, 
  *
  * Rows whose target is ignore_index take part in nothing: whatever their
  * logits, log-probabilities, advantages or teacher entries hold (NaN
- * included), their outputs are 0.  Reductions are those of
+ * included), their outputs are 0.  So are those of a row whose target lies
+ * outside [0, V), where V is given; it sets FLCE_ERR_TARGET_OUT_OF_RANGE in
+ * d_status and still counts in n.  Reductions are those of
  * flce_forward_backward_ex: the loss is sum_i s_i L_i over the other rows with
  * s_i = 1/n, 1 or grad_row_scale[i].  A mean over each answer's tokens and
  * then over the answers is NONE with s_i = 1 / (answers * tokens of i's answer).
@@ -357,8 +359,7 @@ flce_status_t flce_clipped_policy(const float* d_row_loss, const int32_t* y, int
  * [1e-6, 1e6].  d_logp, d_entropy and
  * d_kl (DEVICE fp32 [N]) receive lp, H and kl, 0 on ignored rows.  A logit of
  * -infinity is a vocabulary entry of probability 0; lower finite logits than
- * -2^40 count as -2^40.  Targets outside [0, V) set
- * FLCE_ERR_TARGET_OUT_OF_RANGE in d_status and count as ignored in the sums.
+ * -2^40 count as -2^40.
  * workspace: flce_ce_workspace_size(N, V) bytes.  Asynchronous; may be
  * captured in a CUDA graph. */
 flce_status_t flce_policy_loss(const void* logits, int32_t dtype, int64_t ld, const int32_t* y, int64_t N, int64_t V,

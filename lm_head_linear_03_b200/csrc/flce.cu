@@ -587,11 +587,15 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
                                                    reinterpret_cast<int*>(ws + L.tile_cnt));
     prof_end(stream, slot);
     if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
+    // Without its target's logit a row has neither a policy loss nor an upstream
+    // weight: the post-training heads leave such rows out, as the same losses on
+    // given logits do.
+    const int out_of_range = own ? ignore_index : target_elsewhere(ignore_index);
     prof_begin(stream, KIND_ORDER, &slot);
     flce_row_order_kernel<<<P.tiles_m, CM, 0, stream>>>(
         y, opt.grad_row_scale, static_cast<int>(N), P.tiles_m, ignore_index,
         reinterpret_cast<const int*>(ws + L.tile_cnt), L.packed ? 1 : 0, static_cast<int>(opt.v0),
-        static_cast<int>(V), static_cast<int>(opt.V_total ? opt.V_total : V),
+        static_cast<int>(V), static_cast<int>(opt.V_total ? opt.V_total : V), out_of_range,
         reinterpret_cast<int*>(ws + L.tile_valid), perm, y_perm, g_perm, &ctrl->reordered, &ctrl->n_rows, d_status);
     prof_end(stream, slot);
     if (cudaGetLastError() != cudaSuccess) return cuda_fail(__LINE__);
@@ -680,7 +684,8 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     c.reduction = opt.reduction;
     c.grad_row_scale = g_rows;
     c.row_loss = opt.row_loss;
-    c.mean_count = opt.mean_count;
+    // rows left out for their target are still counted in the mean
+    c.mean_count = own && !opt.mean_count ? &ctrl->n_rows : opt.mean_count;
     c.mode = opt.combine;
     c.shards = opt.shards;
     c.all_lse = opt.all_lse;

@@ -1581,11 +1581,14 @@ __global__ void __launch_bounds__(CM)
 // Every CTA computes the same totals from `tile_cnt`, so they all decide alike.
 // Targets are checked against the whole vocabulary [0, V_total) and stored
 // relative to this call's W rows [v0, v0 + V): a target outside them (held by
-// another vocabulary shard) becomes TARGET_ELSEWHERE, which no column matches.
+// another vocabulary shard) becomes target_elsewhere, which no column matches.
+// One outside the whole vocabulary is reported and becomes `out_of_range`:
+// target_elsewhere too, or ignore_index where such a row takes part in nothing
+// (it still counts in n_rows_out and in the tiles' counts).
 __global__ void __launch_bounds__(CM)
     flce_row_order_kernel(const int32_t* y, const float* g, int N, int TM, int ignore_index, const int* tile_cnt,
-                          int allow, int v0, int V, int V_total, int* tile_valid, int* perm, int32_t* y_perm,
-                          float* g_perm, int* reordered_out, int* n_rows_out, int* status) {
+                          int allow, int v0, int V, int V_total, int out_of_range, int* tile_valid, int* perm,
+                          int32_t* y_perm, float* g_perm, int* reordered_out, int* n_rows_out, int* status) {
   const int t = blockIdx.x;
   int total = 0, nonempty = 0, before = 0;
   for (int i = threadIdx.x; i < TM; i += CM) {
@@ -1624,8 +1627,12 @@ __global__ void __launch_bounds__(CM)
     rank_v += i < w ? wrank[i] : 0;
   }
   const bool reorder = allow != 0 && (total + CM - 1) / CM < nonempty;
-  if (v && (yr < 0 || yr >= V_total)) raise_status(status, ST_TARGET_OUT_OF_RANGE);
-  const int yl = !v ? ignore_index : (yr >= v0 && yr - v0 < V) ? yr - v0 : target_elsewhere(ignore_index);
+  const bool bad = v && (yr < 0 || yr >= V_total);
+  if (bad) raise_status(status, ST_TARGET_OUT_OF_RANGE);
+  const int yl = !v                        ? ignore_index
+                 : bad                     ? out_of_range
+                 : yr >= v0 && yr - v0 < V ? yr - v0
+                                           : target_elsewhere(ignore_index);
   if (in) {
     int dest = r;
     if (reorder) {

@@ -42,3 +42,58 @@ def test_clusters_repeat_their_bits(N, V):
     for _ in range(100):
         for call, w in zip(calls, want):
             assert all(torch.equal(a, b) for a, b in zip(call(), w))
+
+
+# ------------------------------------- targets outside the vocabulary, through the head --
+
+
+@pytest.mark.parametrize("reorder", [False, True])
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+def test_heads_with_targets_out_of_range(reduction, reorder):
+    """Reported, and without a part in anything but the mean's count, whatever the
+    row's vectors and the workspace hold: on a workspace of NaN, and on the same
+    one again."""
+    F = _lib()
+    N, H, V, K = 700, 64, 3000, 20
+    X, W, Z, y, old, adv, ref = _head(N, H, V, seed=6, ign=0.6 if reorder else 0.2)
+    ids, u = teacher_case(N, V, K, seed=6)
+    scale = torch.randn(N, generator=torch.Generator().manual_seed(1)) if reduction == "none" else None
+    bad = torch.tensor([3, 257, N - 1])
+    y[bad] = torch.tensor([V, -7, 2 ** 31 - 1], dtype=torch.int32)
+    valid = y != IGN
+    good = valid.clone()
+    good[bad] = False
+    yg = torch.where(good, y, IGN)
+    share = int(good.sum()) / int(valid.sum()) if reduction == "mean" else 1.0
+    nscale = None if scale is None else _np(scale)
+    for t in (old, adv, ref, u) + (() if scale is None else (scale,)):
+        t[bad] = math.nan
+    d = _cuda(X, W, y)
+    kw = dict(reduction=reduction, grad_row_scale=None if scale is None else scale.cuda())
+    off = (~good).cuda()
+
+    def check(f, args, size, reference, own):
+        loss0, G, rows0 = reference
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        first = f(*d, *args, workspace=ws, **own, **kw)
+        again = f(*d, *args, workspace=ws, **own, **kw)
+        loss, status, rows, dX, dW = first
+        assert status.item() == 4
+        if reorder:
+            assert F.row_order_info(ws)[0]
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+        _close(_np(rows), rows0, 1e-4 * (1 + np.abs(rows0)), "rows")
+        assert not rows[off].any() and not dX[off].any()
+        s = np.abs(O.row_scale(good.numpy(), reduction, nscale)) * share
+        _close(loss.item(), loss0 * share, (s * (1 + np.abs(rows0)) * (1 + np.abs(np.nan_to_num(_np(adv))))).sum() * 2e-4, "loss")
+        assert_grad_close(_np(dX), G @ _np(W) * share, "dX")
+        assert_grad_close(_np(dW), G.T @ _np(X) * share, "dW")
+        fl, _, frows, _, _ = f(*d, *args, workspace=ws, grads=False, **own, **kw)
+        assert torch.equal(fl, loss) and torch.equal(frows, rows)
+
+    p = O.policy_reference(Z, yg, old, adv, ref, 0.2, 0.28, 0.05, reduction=reduction, grad_row_scale=nscale)
+    check(F.policy_forward_backward, _cuda(old, adv), F.policy_workspace_size(N, H, V, reorder), p[:3],
+          dict(ref_logp=ref.cuda(), clip_high=0.28, kl_coef=0.05))
+    t = O.distill_reference(Z, yg, ids, u, None, 1.0, 1.0, 0.5, reduction=reduction, grad_row_scale=nscale)
+    check(F.distill_forward_backward, _cuda(ids, u), F.distill_workspace_size(N, H, V, K, reorder), t,
+          dict(ce_weight=0.5, row_loss=True))
