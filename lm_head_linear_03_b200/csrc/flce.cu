@@ -843,8 +843,9 @@ flce_status_t check_reduction(int32_t r) {
 
 bool is_finite(double x) { return x - x == 0.0; }
 
-// Within this range no product of a logit's difference with 1 / T leaves fp32
-// where the logits are at least -2^40, which the policy loss raises them to.
+// Within this range a difference of logits that matters (up to some 150 T) and
+// its product with 1 / T are fp32 numbers, and what the policy loss raises lower
+// logits to (-2^40) is a million T below 0.
 bool temperature_ok(double t) { return t >= 1e-6 && t <= 1e6; }
 
 // The policy loss's clip widths and KL weight.

@@ -32,11 +32,11 @@ namespace flce {
 
 constexpr int DISTILL_MAX_K = 1024;
 // Lower logits count as LOGIT_LOWEST in the policy loss, whose sums hold e (z - m):
-// the difference stays finite, so that a probability of 0 adds 0.  A register
-// without a logit holds LOGIT_NONE, which has probability 0 beside any logit.
-// Powers of two: the same value in bf16.
+// the difference is finite whatever finite m is, so that a probability of 0 adds
+// 0.  A register without a logit holds LOGIT_NONE, which has probability 0 beside
+// any logit.  Powers of two: the same value in bf16.
 constexpr float LOGIT_LOWEST = -0x1p40f, LOGIT_NONE = -0x1p42f;
-constexpr float NEG_BIG = -1e4f;  // exponents below this are 0 in every format; finite, so that 0 * it is 0
+constexpr double NEG_BIG = -1e4;  // a power of two of this exponent is 0 in every format
 
 // ------------------------------------------------------- logits by type --
 
@@ -80,7 +80,7 @@ struct LogitTraits<__half> {
     const float2 f = __half22float2(reinterpret_cast<const __half2*>(&v)[i]);
     return f32x2(f.x, f.y);
   }
-  static constexpr bool CLAMPS = false;  // 65504 is too near for that at a high temperature
+  static constexpr bool CLAMPS = false;  // 65504 is too near for that at a high temperature: raised in fp32
   __device__ static void clamp(uint4&) {}
   __device__ static void put(uint4& v, int i, float lo, float hi) { reinterpret_cast<__half2*>(&v)[i] = __floats2half2_rn(lo, hi); }
   using Max = __half2;
@@ -388,7 +388,9 @@ struct LogitArgs {
 
 // A row's running statistics under a reference m, which is the maximum to
 // within RAISE in the exponent: sum of e = 2^((z - m) zs), and for the policy loss
-// the first moment sum e (z - m) zs, for DISTILL2 the sum of 2^((z - m) log2 e).
+// the first moment sum e (z - m), for DISTILL2 the sum of 2^((z - m) log2 e).  The
+// moment takes z - m, which is finite, not the exponent, which a large m or a
+// small temperature takes beyond fp32: e is 0 there, and 0 times infinity is NaN.
 struct RowStat {
   float m, l, t;
 };
@@ -399,7 +401,7 @@ constexpr float RAISE = 60.f;
 // What the gradient needs of a row.
 struct RowCoef {
   float m;       // the row's reference
-  float a, b;    // dense part: e (a + b arg), or a e + b e1 with two softmaxes
+  float a, b;    // dense part: e a + e (z - m) b, or e a + e1 b with two softmaxes
   float c, zy;   // policy: subtracted at the target, and the logit there
 };
 
@@ -577,6 +579,13 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
   for (int k = 0; k < TILE_STAGES; ++k) issue();
 
   auto lifted = [&](float x) { return is_policy(LOSS) ? max_nan(x, LOGIT_LOWEST) : x; };
+  // a pair of logits from a chunk, raised where the packed form could not be
+  auto raised = [&](uint64_t x) {
+    if constexpr (!is_policy(LOSS) || L::CLAMPS) return x;
+    float lo, hi;
+    f32x2_split(x, lo, hi);
+    return f32x2(lifted(lo), lifted(hi));
+  };
   const float none = is_policy(LOSS) ? LOGIT_NONE : -INFINITY;
   const uint64_t zs2 = f32x2(a.zs, a.zs), one2 = f32x2(LOG2E, LOG2E);
   int parity = 0;
@@ -669,10 +678,10 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
       if (!__any_sync(0xffffffffu, (lane_top - ref) * steep > RAISE)) return;
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) lane_top = fmaxf(lane_top, __shfl_xor_sync(0xffffffffu, lane_top, s));
-      const float d = (ref - lane_top) * a.zs, f = ex2_approx(d);
+      const float d = ref - lane_top, f = ex2_approx(d * a.zs);
       const uint64_t f2 = f32x2(f, f);
       if constexpr (is_policy(LOSS)) {
-        const float df = fmaxf(d, NEG_BIG);
+        const float df = f == 0.f ? 0.f : d;  // l2 d might overflow, and what it is added to ends as 0
         t2 = mul2(f2, fma2(l2, f32x2(df, df), t2));
       }
       if constexpr (LOSS == LOSS_DISTILL2) {
@@ -684,17 +693,11 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
     };
     auto fold = [&](uint64_t x) {
       const uint64_t d0 = add2(x, f32x2(-ref, -ref));
-      uint64_t d = mul2(d0, zs2);
       float lo, hi;
-      f32x2_split(d, lo, hi);
-      if constexpr (is_policy(LOSS) && !L::CLAMPS) {  // finite, so that a probability of 0 adds 0 to the entropy
-        lo = max_nan(lo, NEG_BIG);
-        hi = max_nan(hi, NEG_BIG);
-        d = f32x2(lo, hi);
-      }
+      f32x2_split(mul2(d0, zs2), lo, hi);
       const uint64_t e = f32x2(ex2_approx(lo), ex2_approx(hi));
       l2 = add2(l2, e);
-      if constexpr (is_policy(LOSS)) t2 = fma2(e, d, t2);
+      if constexpr (is_policy(LOSS)) t2 = fma2(e, d0, t2);
       if constexpr (LOSS == LOSS_DISTILL2) {
         f32x2_split(mul2(d0, one2), lo, hi);
         t2 = add2(t2, f32x2(ex2_approx(lo), ex2_approx(hi)));
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
         if (has(u)) {
           if constexpr (is_policy(LOSS)) L::clamp(v[u]);
 #pragma unroll
-          for (int i = 0; i < EPC / 2; ++i) fold(L::pair(v[u], i));
+          for (int i = 0; i < EPC / 2; ++i) fold(raised(L::pair(v[u], i)));
         }
       }
     };
@@ -777,11 +780,11 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
       for (int r = lane; r < records; r += 32) {
         const float4 v = rec[parity][r];
         const double gap = static_cast<double>(v.x) - static_cast<double>(ref_max);
-        const double d = fmax(gap * static_cast<double>(a.zs), static_cast<double>(NEG_BIG)), f = exp2(d);
+        const double f = exp2(fmax(gap * static_cast<double>(a.zs), NEG_BIG));
         sum_l += f * static_cast<double>(v.y);
-        if constexpr (is_policy(LOSS)) sum_t += f * (static_cast<double>(v.z) + d * static_cast<double>(v.y));
+        if constexpr (is_policy(LOSS)) sum_t += f * (static_cast<double>(v.z) + gap * static_cast<double>(v.y));
         if constexpr (LOSS == LOSS_DISTILL2)
-          sum_t += exp2(fmax(gap * static_cast<double>(LOG2E), static_cast<double>(NEG_BIG))) * static_cast<double>(v.z);
+          sum_t += exp2(fmax(gap * static_cast<double>(LOG2E), NEG_BIG)) * static_cast<double>(v.z);
         top = fmaxf(top, v.w);
       }
 #pragma unroll
@@ -795,21 +798,22 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
       const double m = static_cast<double>(ref_max);
       const double inv_l = 1.0 / sum_l;
       double lnL = log(sum_l);
-      // zs is off by zs_off of itself: d ln L / d ln zs = ln 2 E[arg]
-      if (is_policy(LOSS)) lnL -= a.zs_off * LN2 * sum_t * inv_l;
+      const double mean = sum_t * inv_l;  // policy: E[z - m]
+      // zs is off by zs_off of itself: d ln L / d ln zs = E[z - m] / T
+      if (is_policy(LOSS)) lnL -= a.zs_off * a.inv_T * mean;
       const float zy = L::load(&zy_raw);
       double total = 0.0;
       RowCoef c{ref_max, 0.f, 0.f, 0.f, 0.f};
       if constexpr (is_policy(LOSS)) {
         const double lp = (static_cast<double>(zy == -INFINITY ? zy : lifted(zy)) - m) * a.inv_T - lnL;
-        const double H = lnL - sum_t * inv_l * LN2;
+        const double H = lnL - mean * a.inv_T;
         const PolicyRow r = policy_row(a.pol, pin, lp);
         total = r.loss;
         double a0 = -r.dlogp, a1 = 0.0;
         if (a.ent_coef != 0.0) {
           total -= a.ent_coef * H;
           a0 += a.ent_coef * (H - lnL);
-          a1 = a.ent_coef * LN2;
+          a1 = a.ent_coef * a.inv_T;
         }
         const double f = scale * a.inv_T;
         c.a = static_cast<float>(a0 * f * inv_l);
@@ -866,17 +870,14 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
       const RowCoef c = coefs[parity];
       const uint64_t neg_m2 = f32x2(-c.m, -c.m), a2 = f32x2(c.a, c.a), b2 = f32x2(c.b, c.b);
       auto dense2 = [&](uint64_t x) {
-        const uint64_t d0 = add2(x, neg_m2);
-        uint64_t d = mul2(d0, zs2);
+        const uint64_t d0 = add2(LOSS == LOSS_POLICY_ENT ? raised(x) : x, neg_m2);
         float lo, hi;
-        f32x2_split(d, lo, hi);
-        if constexpr (LOSS == LOSS_POLICY_ENT && !L::CLAMPS) {
-          lo = max_nan(lo, NEG_BIG);
-          hi = max_nan(hi, NEG_BIG);
-          d = f32x2(lo, hi);
-        }
+        f32x2_split(mul2(d0, zs2), lo, hi);
         const uint64_t e = f32x2(ex2_approx(lo), ex2_approx(hi));
-        if constexpr (LOSS == LOSS_POLICY_ENT) return mul2(e, fma2(b2, d, a2));
+        // b (z - m) may overflow where e is 0, with a logit near the largest fp32 value:
+        // e (z - m) comes first.  4096 x 128256 takes 1% longer than with e (a + b (z - m)),
+        // as with a choice between the two per row.
+        if constexpr (LOSS == LOSS_POLICY_ENT) return fma2(mul2(e, d0), b2, mul2(e, a2));
         if constexpr (LOSS == LOSS_DISTILL2) {
           f32x2_split(mul2(d0, one2), lo, hi);
           return fma2(f32x2(ex2_approx(lo), ex2_approx(hi)), b2, mul2(e, a2));

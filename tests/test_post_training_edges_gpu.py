@@ -10,7 +10,7 @@ import torch
 from oracle import flce_oracle as O
 from test_parity_gpu import assert_grad_close
 from test_post_training import IGN, policy_case, teacher_case
-from test_post_training_gpu import DT, EPS32, _check_distill, _check_policy, _close, _cuda, _delta, _head, _lib, _np
+from test_post_training_gpu import DT, EPS32, TINY, _check_distill, _check_policy, _close, _cuda, _delta, _head, _lib, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +97,48 @@ def test_heads_with_targets_out_of_range(reduction, reorder):
     t = O.distill_reference(Z, yg, ids, u, None, 1.0, 1.0, 0.5, reduction=reduction, grad_row_scale=nscale)
     check(F.distill_forward_backward, _cuda(ids, u), F.distill_workspace_size(N, H, V, K, reorder), t,
           dict(ce_weight=0.5, row_loss=True))
+
+
+# ---------------------------------------------------------------- huge logits --
+
+
+@pytest.mark.parametrize("ent", [0.0, 0.1])
+@pytest.mark.parametrize("T", [1e-6, 0.01, 1.0, 1e3, 1e6])
+@pytest.mark.parametrize("dtype", DT, ids=["bf16", "fp16", "fp32"])
+def test_policy_logits_up_to_the_largest_value(dtype, T, ent, monkeypatch):
+    """A token forced by the type's largest value, alone, at the end of a row, in
+    several places, beside masked entries and against ordinary ones: the softmax
+    is one token's (or an even one), its entropy 0 (or a logarithm)."""
+    if dtype is torch.float16 and T < 1e-3:
+        pytest.skip("gradients of |A| / (N T) are beyond fp16's 65504")
+    N, V = 8, 3001
+    Z, y, _, adv, _ = policy_case(N, V, seed=3, dtype=dtype, ign=0.0)
+    big = torch.finfo(dtype).max
+    Z[0, 7] = big
+    Z[1, V - 1] = big
+    Z[2, 40:44] = big
+    Z[3] = Z[3].masked_fill(torch.rand(V, generator=torch.Generator().manual_seed(1)) < 0.5, -math.inf)
+    Z[3, 1000] = big
+    Z[4] = torch.finfo(dtype).min
+    Z[4, 2000] = big
+    Z[5] = big
+    Z[6, 2999], Z[6, 5] = big, 0.75 * big
+    top = Z.float().argmax(1).to(torch.int32)
+    y = top if T < 1 else torch.where(torch.arange(N) % 2 == 0, top, y)  # a lower T takes -max / T out of fp32
+    # exponentials below 2^-126 are 0; each has the factor (|A| + ent (H + 88)) / T <= 100 / T, with |A| < 5
+    monkeypatch.setitem(TINY, dtype, max(TINY[dtype], 100 / T * 2.0 ** -126))
+    _check_policy(Z, y, None, adv, None, kl=0.0, ent=ent, T=T)
+    _check_policy(Z, y, None, adv, None, kl=0.0, ent=ent, T=T, grad="inplace", lead=1, pad=4)
+
+
+@pytest.mark.parametrize("dtype", DT, ids=["bf16", "fp16", "fp32"])
+def test_distill_logits_up_to_the_largest_value(dtype):
+    N, V = 6, 3001
+    Z, y, *_ = policy_case(N, V, seed=4, dtype=dtype, ign=0.0)
+    ids, u = teacher_case(N, V, 3, seed=4, padded=False)
+    Z[:3, 11] = torch.finfo(dtype).max
+    Z[2, 2000] = torch.finfo(dtype).max
+    ids[:3] = torch.tensor([11, -1, -1], dtype=torch.int32)
+    y[:3] = 11
+    _check_distill(Z, y, ids, u, T=2.0, ce=0.5)
+    _check_distill(Z, y, ids, u, ce=0.5)
