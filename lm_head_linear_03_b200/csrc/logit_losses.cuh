@@ -876,8 +876,9 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
         const uint64_t e = f32x2(ex2_approx(lo), ex2_approx(hi));
         // b (z - m) may overflow where e is 0, with a logit near the largest fp32 value:
         // e (z - m) comes first.  4096 x 128256 takes 1% longer than with e (a + b (z - m)),
-        // as with a choice between the two per row.
-        if constexpr (LOSS == LOSS_POLICY_ENT) return fma2(mul2(e, d0), b2, mul2(e, a2));
+        // as with a choice between the two per row.  fp16 has no such logits.
+        if constexpr (LOSS == LOSS_POLICY_ENT && L::CLAMPS) return fma2(mul2(e, d0), b2, mul2(e, a2));
+        if constexpr (LOSS == LOSS_POLICY_ENT) return mul2(e, fma2(b2, d0, a2));
         if constexpr (LOSS == LOSS_DISTILL2) {
           f32x2_split(mul2(d0, one2), lo, hi);
           return fma2(f32x2(ex2_approx(lo), ex2_approx(hi)), b2, mul2(e, a2));
