@@ -414,8 +414,10 @@ flce_status_t flce_policy_forward_backward(const uint16_t* X, const uint16_t* W,
 
 /* Distillation through the head, z = X W^T never stored.  Loss and teacher
  * arguments as flce_distill_topk, except that ce_weight needs temperature 1
- * (FLCE_ERR_UNSUPPORTED otherwise: a logit tile is turned into one softmax);
- * other arguments as flce_forward_backward_ex.  workspace:
+ * (FLCE_ERR_UNSUPPORTED otherwise: a logit tile is turned into one softmax).
+ * The logits are fp32 sums of H products, and their rounding reaches the
+ * probabilities divided by the temperature; nothing else grows as it falls.
+ * Other arguments as flce_forward_backward_ex.  workspace:
  * flce_distill_workspace_size bytes, as flce_policy_workspace_size with the
  * rows' entry lists behind it (the same query with V = 1 gives the least that a
  * call takes). */

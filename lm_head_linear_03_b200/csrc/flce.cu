@@ -157,7 +157,7 @@ CeLayout ce_ws_layout(int64_t N) {
 // Area behind the head's workspace for a distillation call: each row's sorted
 // list of vocabulary entries and its constants.
 struct ListLayout {
-  size_t list, count, dense, kconst, klse, part_dot, total;
+  size_t list, count, dense, kconst, klse, ksum, part_dot, total;
 };
 ListLayout list_layout(int64_t N, int64_t K, size_t off) {
   ListLayout L{};
@@ -172,6 +172,7 @@ ListLayout list_layout(int64_t N, int64_t K, size_t off) {
   L.dense = take(n * 4);
   L.kconst = take(n * 8);
   L.klse = take(n * 8);
+  L.ksum = take(n * 8);
   L.part_dot = take(n * MAX_SPLITS * 8);
   L.total = off;
   return L;
@@ -568,11 +569,13 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     t.list_dense = reinterpret_cast<float*>(ws + E.dense);
     t.list_const = reinterpret_cast<double*>(ws + E.kconst);
     t.list_lse = reinterpret_cast<double*>(ws + E.klse);
+    t.list_sum = reinterpret_cast<double*>(ws + E.ksum);
     t.status = d_status;
     a.list = t.list;
     a.part_dot = reinterpret_cast<double*>(ws + E.part_dot);
     a.list_count = t.list_count;
     a.list_dense = t.list_dense;
+    a.row_max = zy;
     a.list_stride = in.K + 1;
     a.zs = static_cast<float>(1.0 / (LN2 * in.temperature));
   }
@@ -701,7 +704,10 @@ flce_status_t enqueue(const uint16_t* X, const uint16_t* W, const int32_t* y, in
     if (opt.teacher) {
       c.list_const = t.list_const;
       c.list_lse = t.list_lse;
+      c.list_sum = t.list_sum;
       c.part_dot = a.part_dot;
+      c.row_max = zy;
+      c.zs = a.zs;
     }
     const int grid = static_cast<int>((N + COMBINE_THREADS - 1) / COMBINE_THREADS);
     size_t slot;

@@ -127,10 +127,10 @@ struct GemmArgs {
   int split_off;          // pass 1: first partial slot of this launch's splits
   int Vc;                 // pass 2: chunk width = row stride of the G buffer
   const int32_t* y;
-  float* part_m;          // [splits][N] running max, log2 units
-  float* part_l;          // [splits][N] running sum of 2^(s - m)
+  float* part_m;          // [splits][N] running max, log2 units (LIST: of the logits themselves)
+  float* part_l;          // [splits][N] running sum of 2^(s - m) (LIST: of 2^((z - m) zs))
   float* zy;              // [N] target logit
-  const float* lse2;      // [N] log2-sum-exp2 of z*log2(e)
+  const float* lse2;      // [N] log2-sum-exp2 of z*log2(e) (LIST: log2 of the row's sum under row_max)
   const float* inv_n;     // 1 / n_valid (0 when n_valid = 0)
   uint16_t* G;            // [N][Vc] bf16
   uint16_t* dW;           // [V][H] bf16
@@ -145,11 +145,13 @@ struct GemmArgs {
   const float* row_mult;         // a further factor of each row's G (derivative of a loss of l_i), or null
   // Distillation (the kernels' LIST instantiations): each row's entries of the
   // vocabulary where G is not the softmax alone, ascending by id, and the
-  // softmax taken at a temperature
+  // softmax taken at a temperature.  That may be low: exponents are (z - m) zs,
+  // not z zs - m zs, whose terms would be rounded to 2^-24 of |z| zs each.
   const int2* list;              // [N][list_stride] id, coefficient c (fp32 bits) subtracted there (times the row's weight)
   double* part_dot;              // [splits][N] pass 1: sum of c z over the entries in the split
   const int* list_count;         // [N]
   const float* list_dense;       // [N] factor of the softmax in G (times the row's weight)
+  const float* row_max;          // [N] the row's largest logit
   int list_stride;
   float zs;                      // log2(e) / temperature
   const int* tile_valid;         // [ceil(N/256)] valid rows per 256-row token tile (prep kernel)
@@ -265,7 +267,7 @@ struct LseState {
 template <bool LIST>
 __device__ __forceinline__ void epi_lse_tile(const GemmArgs& a, uint32_t taddr, int nb, LseState& st) {
   const int col_base = nb * BN;
-  const float zs = LIST ? a.zs : LOG2E;
+  auto exponent = [&](float d) { return LIST ? d * a.zs : d; };  // of a difference of s
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
     uint32_t r[32];
@@ -297,19 +299,19 @@ __device__ __forceinline__ void epi_lse_tile(const GemmArgs& a, uint32_t taddr, 
     float cmax = -INFINITY;
 #pragma unroll
     for (int t = 0; t < 32; ++t) {
-      s[t] = (t < lim) ? __uint_as_float(r[t]) * zs : -INFINITY;
+      s[t] = (t < lim) ? __uint_as_float(r[t]) * (LIST ? 1.f : LOG2E) : -INFINITY;
       cmax = fmaxf(cmax, s[t]);
     }
     const float new_m = fmaxf(st.run_m, cmax);
     float acc0 = 0.f, acc1 = 0.f, acc2 = 0.f, acc3 = 0.f;
 #pragma unroll
     for (int t = 0; t < 32; t += 4) {
-      acc0 += ex2_approx(s[t + 0] - new_m);
-      acc1 += ex2_approx(s[t + 1] - new_m);
-      acc2 += ex2_approx(s[t + 2] - new_m);
-      acc3 += ex2_approx(s[t + 3] - new_m);
+      acc0 += ex2_approx(exponent(s[t + 0] - new_m));
+      acc1 += ex2_approx(exponent(s[t + 1] - new_m));
+      acc2 += ex2_approx(exponent(s[t + 2] - new_m));
+      acc3 += ex2_approx(exponent(s[t + 3] - new_m));
     }
-    st.run_l = st.run_l * ex2_approx(st.run_m - new_m) + ((acc0 + acc1) + (acc2 + acc3));
+    st.run_l = st.run_l * ex2_approx(exponent(st.run_m - new_m)) + ((acc0 + acc1) + (acc2 + acc3));
     st.run_m = new_m;
   }
 }
@@ -408,8 +410,9 @@ __device__ __forceinline__ void epi_grad_tile(const GemmArgs& a, int vbase, uint
   const float l2 = valid ? a.lse2[row] : 0.f;
   float scale = valid ? row_weight(a.reduction, a.inv_n, a.grad_row_scale, row) : 0.f;
   if (a.row_mult && valid) scale *= a.row_mult[row];
-  const float zs = LIST ? a.zs : LOG2E;
+  const float m = LIST && valid ? a.row_max[row] : 0.f;
   const float dense = LIST && valid ? scale * a.list_dense[row] : scale;
+  auto prob = [&](float z) { return ex2_approx(LIST ? fmaf(z - m, a.zs, -l2) : fmaf(z, LOG2E, -l2)); };
   const int wrow0 = row0 + (row_local & ~31);
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
@@ -421,7 +424,7 @@ __device__ __forceinline__ void epi_grad_tile(const GemmArgs& a, int vbase, uint
     stage_and_store(es, lane, mapG, nb * BN + c * 32, wrow0, l2_evict_normal(), [&](float (&g)[32]) {
 #pragma unroll
       for (int t = 0; t < 32; ++t)
-        g[t] = (valid && t < lim) ? ex2_approx(fmaf(__uint_as_float(r[t]), zs, -l2)) * dense : 0.f;
+        g[t] = (valid && t < lim) ? prob(__uint_as_float(r[t])) * dense : 0.f;
       if constexpr (LIST) {
         while (walk.next.x < colg0 + 32) {
           const int o = walk.next.x - colg0;
@@ -1751,10 +1754,16 @@ struct CombineArgs {
   PolicyArgs pol;
   float* logp;      // [N]
   float* row_mult;  // [N] d L_i / d l_i; may be zy itself
-  // Distillation: the row's loss is list_const + list_lse lse - the sum of part_dot (all null otherwise)
+  // Distillation (all null otherwise): with the row's maximum m and ln L of its sum
+  // under m, its loss is list_const + list_lse ln L + list_sum m - the sum of
+  // part_dot.  list_sum adds the coefficients as part_dot has them, rounded, so
+  // that the last two leave a sum of c (m - z), however large m is.
   const double* list_const;
   const double* list_lse;
+  const double* list_sum;
   const double* part_dot;  // [splits][N]
+  float* row_max;          // [N] output; may be zy itself, which such a call has no use for
+  float zs;
   const int* perm;  // row of the caller behind each row of y, part_m, ... (token-row order)
   const int* mean_count;  // optional: divide the mean by this count instead of n_valid
   const int32_t* y;
@@ -1790,7 +1799,22 @@ __global__ void __launch_bounds__(COMBINE_THREADS) flce_combine_kernel(const Com
     const int yi = a.y[i];
     const bool valid = yi != a.ignore_index;
     float l2, zyi;
-    if (a.mode == COMBINE_SHARDS_IN) {
+    double ln_l = 0.0, top = 0.0;  // distillation
+    if (a.part_dot) {
+      float M = -INFINITY;
+#pragma unroll 8
+      for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.part_m[static_cast<size_t>(s) * a.N + i]);
+      double L = 0.0;
+#pragma unroll 8
+      for (int s = 0; s < a.splits; ++s)
+        L += static_cast<double>(a.part_l[static_cast<size_t>(s) * a.N + i]) *
+             static_cast<double>(exp2f((a.part_m[static_cast<size_t>(s) * a.N + i] - M) * a.zs));
+      top = static_cast<double>(M);
+      ln_l = log(L);
+      l2 = static_cast<float>(ln_l / LN2);
+      zyi = 0.f;
+      a.row_max[i] = M;
+    } else if (a.mode == COMBINE_SHARDS_IN) {
       float M = -INFINITY;
       for (int s = 0; s < a.shards; ++s) M = fmaxf(M, a.all_lse[static_cast<size_t>(s) * a.N + i]);
       float S = 0.f;
@@ -1825,7 +1849,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) flce_combine_kernel(const Com
         double dot = 0.0;
 #pragma unroll 8
         for (int s = 0; s < a.splits; ++s) dot += a.part_dot[static_cast<size_t>(s) * a.N + i];
-        row = a.list_const[i] + a.list_lse[i] * (static_cast<double>(l2) * LN2) - dot;
+        row = a.list_const[i] + a.list_lse[i] * ln_l + (a.list_sum[i] * top - dot);
       }
       vi = 1;
       // mean and sum add the plain row losses (the mean divides at the end)

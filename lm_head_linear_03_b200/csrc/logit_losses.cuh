@@ -999,14 +999,16 @@ struct TeacherArgs {
   float* list_dense;
   double* list_const;
   double* list_lse;
+  double* list_sum;
   int* status;
 };
 
 // Each row's entries (the teacher's, and the target when hard labels are mixed
 // in) ascending by id, with the coefficients that the G tiles subtract there,
 // and the row's constants:
-//   L = kd sum q log q + (kd Q + ce) lse - sum_k c_k z_k,  c_k = kd q_k / T + ce [target],
-//   G = s ((kd Q / T + ce) p - c).
+//   L = kd sum q log q + (kd Q + ce) ln L + sum_k c_k (m - z_k),  c_k = kd q_k / T + ce [target],
+//   G = s ((kd Q / T + ce) p - c),
+// with the student's maximum m and its sum L of e^((z - m) / T) (ce needs T = 1).
 // Entries are ranked by counting (id, position) pairs below their own, so the
 // order is the same on every call; equal ids stay separate entries, which the
 // G tiles subtract one after the other.  One CTA per row: counting is K^2 / 128
@@ -1025,7 +1027,7 @@ __global__ void __launch_bounds__(TEACHER_THREADS) flce_teacher_lists_kernel(con
       if (tid == 0) {
         a.list_count[i] = 0;
         a.list_dense[i] = 0.f;
-        a.list_const[i] = a.list_lse[i] = 0.0;
+        a.list_const[i] = a.list_lse[i] = a.list_sum[i] = 0.0;
       }
       continue;
     }
@@ -1049,14 +1051,22 @@ __global__ void __launch_bounds__(TEACHER_THREADS) flce_teacher_lists_kernel(con
     }
     __syncthreads();
     const TeacherShift ts = teacher_shift(s_u, a.K, lane, a.inv_T, a.teacher_lse, src);
-    double Q = 0.0, qlogq = 0.0;
+    auto log_q = [&](int k) { return static_cast<double>(s_u[k]) * a.inv_T - ts.shift; };
+    auto prob = [&](int k) { return expf(static_cast<float>(log_q(k))); };
+    auto coef = [&](int k) {  // c of an entry, as the list holds it
+      return static_cast<float>(k == a.K ? a.ce : ts.any ? static_cast<double>(prob(k)) * a.kd * a.inv_T : 0.0);
+    };
+    double Q = 0.0, qlogq = 0.0, csum = 0.0;
     int count = 0;
     if (tid < 32) {
       for (int k = lane; k < K1; k += 32) {
-        if (s_id[k] != 0x7fffffff) ++count;
+        if (s_id[k] != 0x7fffffff) {
+          ++count;
+          csum += static_cast<double>(coef(k));
+        }
         if (k < a.K && ts.any) {
-          const double lq = static_cast<double>(s_u[k]) * a.inv_T - ts.shift;
-          const float q = expf(static_cast<float>(lq));
+          const double lq = log_q(k);
+          const float q = prob(k);
           Q += q;
           if (!(q == 0.f)) qlogq += static_cast<double>(q) * lq;
         }
@@ -1065,6 +1075,7 @@ __global__ void __launch_bounds__(TEACHER_THREADS) flce_teacher_lists_kernel(con
       for (int o = 16; o > 0; o >>= 1) {
         Q += __shfl_xor_sync(0xffffffffu, Q, o);
         qlogq += __shfl_xor_sync(0xffffffffu, qlogq, o);
+        csum += __shfl_xor_sync(0xffffffffu, csum, o);
         count += __shfl_xor_sync(0xffffffffu, count, o);
       }
       if (lane == 0) {
@@ -1072,6 +1083,7 @@ __global__ void __launch_bounds__(TEACHER_THREADS) flce_teacher_lists_kernel(con
         a.list_dense[i] = static_cast<float>(a.kd * Q * a.inv_T + a.ce);
         a.list_const[i] = a.kd * qlogq;
         a.list_lse[i] = a.kd * Q + a.ce;
+        a.list_sum[i] = csum;
       }
     }
     for (int k = tid; k < K1; k += TEACHER_THREADS) {
@@ -1079,9 +1091,7 @@ __global__ void __launch_bounds__(TEACHER_THREADS) flce_teacher_lists_kernel(con
       if (id == 0x7fffffff) continue;
       int rank = 0;
       for (int j = 0; j < K1; ++j) rank += s_id[j] < id || (s_id[j] == id && j < k) ? 1 : 0;
-      double c = a.ce;
-      if (k < a.K) c = ts.any ? static_cast<double>(expf(static_cast<float>(static_cast<double>(s_u[k]) * a.inv_T - ts.shift))) * a.kd * a.inv_T : 0.0;
-      a.list[out + rank] = make_int2(id, __float_as_int(static_cast<float>(c)));
+      a.list[out + rank] = make_int2(id, __float_as_int(coef(k)));
     }
     __syncthreads();
   }

@@ -142,3 +142,67 @@ def test_distill_logits_up_to_the_largest_value(dtype):
     y[:3] = 11
     _check_distill(Z, y, ids, u, T=2.0, ce=0.5)
     _check_distill(Z, y, ids, u, ce=0.5)
+
+
+# --------------------------------------------- the distillation head's temperatures --
+
+
+@pytest.mark.parametrize("T", [1e-6, 1e-4, 0.02, 1.0, 50.0, 1e3, 1e6])
+def test_distill_head_temperature_range(T):
+    """Logits that are exact sums in fp32, far from 0 and a few temperatures apart:
+    32768 temperatures plus small multiples of one.  Probabilities hang on the
+    differences alone, which the head has exactly."""
+    F = _lib()
+    N, H, V, K = 300, 16, 2100, 8
+    g = torch.Generator().manual_seed(8)
+    step = 2.0 ** round(math.log2(T))
+    X = torch.zeros(N, H)
+    X[:, 0] = 1
+    X[:, 1:4] = torch.randint(-2, 3, (N, 3), generator=g).float()
+    W = torch.zeros(V, H)
+    W[:, 0] = 32768 * step
+    W[:, 1:4] = torch.randint(-3, 4, (V, 3), generator=g).float() * step
+    X, W = X.bfloat16(), W.bfloat16()
+    Z = X.double() @ W.double().T
+    assert torch.equal(Z.float().double(), Z)
+    y = torch.randint(0, V, (N,), generator=g, dtype=torch.int64).to(torch.int32)
+    y[::7] = IGN
+    ids, u = teacher_case(N, V, K, seed=8)
+    ids[3] = -1
+    u = u * step
+    ce = 0.5 if T == 1.0 else 0.0
+    loss, status, rows, dX, dW = F.distill_forward_backward(*_cuda(X, W, y, ids, u), temperature=T, ce_weight=ce, row_loss=True)
+    assert status.item() == 0
+    rloss, G, rrows = O.distill_reference(Z, y, ids, u, None, T, 1.0, ce)
+    # one exponential per probability (argument below 40, 2^-24 of it, 2 steps more) and fp32 coefficients
+    _close(_np(rows), rrows, 1e-5 * (1 + np.abs(rrows)), "row loss")
+    _close(loss.item(), rloss, 1e-5 * (1 + np.abs(rrows)).mean(), "loss")
+    # columns 1 to 3 of dW and dX; column 0 of dX is 32768 temperatures times a sum of 0
+    assert_grad_close(_np(dW)[:, 1:4], (G.T @ _np(X))[:, 1:4], "dW")
+    assert_grad_close(_np(dX)[:, 1:4], (G @ _np(W))[:, 1:4], "dX")
+    fl, _, frows, _, _ = F.distill_forward_backward(*_cuda(X, W, y, ids, u), temperature=T, ce_weight=ce, row_loss=True,
+                                                    grads=False)
+    assert torch.equal(fl, loss) and torch.equal(frows, rows)
+
+
+def test_distill_head_small_loss_at_a_low_temperature():
+    """A teacher that agrees with the student: the loss is a small difference of
+    terms of some 30 / T each."""
+    F = _lib()
+    N, H, V, K, T = 64, 8, 700, 700, 2.0 ** -12
+    g = torch.Generator().manual_seed(9)
+    X = torch.zeros(N, H)
+    X[:, 0], X[:, 1] = 1, torch.randint(1, 3, (N,), generator=g).float()
+    W = torch.zeros(V, H)
+    W[:, 0], W[:, 1] = 32, torch.randint(-2, 3, (V,), generator=g).float() * T
+    X, W = X.bfloat16(), W.bfloat16()
+    Z = (X.double() @ W.double().T).float()
+    y = torch.zeros(N, dtype=torch.int32)
+    ids = torch.stack([torch.randperm(V, generator=g) for _ in range(N)]).to(torch.int32)
+    u = Z.gather(1, ids.long()) - 31            # another constant: the same softmax
+    loss, status, rows, dX, dW = F.distill_forward_backward(*_cuda(X, W, y, ids, u), temperature=T, row_loss=True)
+    assert status.item() == 0
+    _, G, rrows = O.distill_reference(Z, y, ids, u, None, T)
+    assert np.abs(rrows).max() < 1e-10
+    # 700 terms of q (a few 2^-24 of each) times logarithms below 12
+    _close(_np(rows), rrows, 12 * 20 * EPS32, "row loss")
