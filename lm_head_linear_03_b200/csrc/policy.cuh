@@ -43,7 +43,7 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, const Polic
   if (p.ref_logp) {
     const double d = static_cast<double>(in.ref) - lp;
     const double em1 = expm1(d);
-    o.kl = em1 - d;
+    o.kl = isinf(em1) ? em1 : em1 - d;  // lp = -infinity: the estimate's limit, not infinity less infinity
     if (p.kl_coef != 0.0) {
       o.loss += p.kl_coef * o.kl;
       o.dlogp -= p.kl_coef * em1;

@@ -206,3 +206,35 @@ def test_distill_head_small_loss_at_a_low_temperature():
     assert np.abs(rrows).max() < 1e-10
     # 700 terms of q (a few 2^-24 of each) times logarithms below 12
     _close(_np(rows), rrows, 12 * 20 * EPS32, "row loss")
+
+
+# ------------------------------------------------------------ infinite results --
+
+
+def test_infinite_results_are_infinite():
+    """A target (or a teacher's entry) of probability 0: lp is -infinity, the KL
+    estimate and the row's loss +infinity, and the others stay as they are."""
+    F = _lib()
+    Z, y, old, adv, ref = policy_case(6, 100, seed=11, ign=0.0)
+    ids, u = teacher_case(6, 100, 3, seed=11, padded=False)
+    Z[1, y[1].long()] = -math.inf
+    _, _, lp, H, kl, g = F.policy_loss(*_cuda(Z, y, old, adv), ref_logp=ref.cuda())
+    assert lp[1].item() == -math.inf and kl[1].item() == math.inf and torch.isfinite(H).all() and torch.isfinite(g).all()
+    _, _, rlp, rH, _ = O.policy_reference(Z, y, old, adv, None)
+    _close(_np(H), rH, _delta(100) * (1 + rH), "entropy")
+    keep = [0, 2, 3, 4, 5]
+    _close(_np(lp)[keep], rlp[keep], _delta(100) + np.abs(rlp[keep]) * EPS32, "logp")
+    Z[4, ids[4, 0].long()] = -math.inf
+    _, _, rows, g = F.distill_topk(*_cuda(Z, y, ids, u), row_loss=True)
+    want = [i for i in range(6) if Z[i, ids[i].long()].isneginf().any()]
+    assert torch.isposinf(rows).nonzero().flatten().tolist() == want and torch.isfinite(g).all()
+
+
+def test_policy_rows_of_probability_zero():
+    F = _lib()
+    l, y = torch.tensor([math.inf, 1.0, 2.0]), torch.tensor([1, 2, IGN], dtype=torch.int32)
+    old, adv, ref = torch.tensor([-1.0, -1.0, 0.0]), torch.tensor([1.0, 1.0, 1.0]), torch.tensor([-2.0, -1.5, 0.0])
+    loss, rows, kl, w, status = F.clipped_policy(*_cuda(l, y, old, adv), ref_logp=ref.cuda())
+    assert kl.tolist()[0] == math.inf and kl.tolist()[2] == 0.0 and status.item() == 0
+    assert abs(kl[1].item() - (math.exp(-0.5) - 0.5)) <= 2 * EPS32
+    assert rows.tolist() == [0.0, -1.0, 0.0] and w.tolist() == [0.0, 0.5, 0.0] and loss.item() == -0.5
