@@ -238,3 +238,116 @@ def test_policy_rows_of_probability_zero():
     assert kl.tolist()[0] == math.inf and kl.tolist()[2] == 0.0 and status.item() == 0
     assert abs(kl[1].item() - (math.exp(-0.5) - 0.5)) <= 2 * EPS32
     assert rows.tolist() == [0.0, -1.0, 0.0] and w.tolist() == [0.0, 0.5, 0.0] and loss.item() == -0.5
+
+
+# --------------------------------------------------------- what other tests leave open --
+
+
+def test_a_bad_row_leaves_the_others_alone():
+    """NaN and infinity in a row make its own results NaN and no other row's."""
+    F = _lib()
+    Z, y, old, adv, ref = policy_case(12, 300, seed=10, ign=0.0)
+    ids, u = teacher_case(12, 300, 5, seed=10)
+    clean = F.policy_loss(*_cuda(Z, y, old, adv), entropy_coef=0.1), F.distill_topk(*_cuda(Z, y, ids, u), row_loss=True)
+    Z[2, 5] = math.nan
+    Z[3] = -math.inf
+    Z[4, 7] = math.inf
+    bad = torch.tensor([2, 3, 4])
+    good = torch.tensor([i for i in range(12) if i not in (2, 3, 4)])
+    got = F.policy_loss(*_cuda(Z, y, old, adv), entropy_coef=0.1), F.distill_topk(*_cuda(Z, y, ids, u), row_loss=True)
+    for was, now in ((clean[0][2:4] + clean[0][5:], got[0][2:4] + got[0][5:]), (clean[1][2:], got[1][2:])):
+        for a, b in zip(was, now):
+            assert torch.equal(a.cpu()[good], b.cpu()[good])
+    assert torch.isnan(got[0][5].cpu()[bad]).all() and torch.isnan(got[0][0]).all() and torch.isnan(got[1][0]).all()
+    assert torch.isnan(got[1][3].cpu()[bad]).all()
+
+
+@pytest.mark.parametrize("T", [1e-6, 1e-3, 1e3, 1e6])
+@pytest.mark.parametrize("dtype", DT, ids=["bf16", "fp16", "fp32"])
+def test_gradients_over_the_temperature_range(T, dtype):
+    if dtype is torch.float16 and (T < 1e-3 or T > 1e3):
+        pytest.skip("logits of this size are not fp16 numbers")
+    g = torch.Generator().manual_seed(3)
+    step = 2.0 ** round(math.log2(T))
+    Z = (torch.randint(-6, 7, (9, 300), generator=g).double() * step).to(dtype)
+    mask = torch.rand(9, 300, generator=g) < 0.3
+    mask[:, 0] = False
+    Z = Z.masked_fill(mask, -math.inf)
+    y = torch.zeros(9, dtype=torch.int32)
+    adv = torch.randn(9, generator=g)
+    _check_policy(Z, y, None, adv, None, kl=0.0, ent=0.1, T=T)
+    ids, u = teacher_case(9, 300, 5)
+    ids = torch.where(mask.gather(1, ids.long().clamp(min=0)), -1, ids).to(torch.int32)
+    _check_distill(Z, y, ids, (u * step).float(), T=T)
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+def test_loss_of_heads_with_reordered_rows(reduction):
+    F = _lib()
+    N, H, V, K = 1300, 64, 3000, 20
+    X, W, Z, y, old, adv, ref = _head(N, H, V, seed=4, ign=0.6)
+    ids, u = teacher_case(N, V, K, seed=4)
+    scale = torch.randn(N, generator=torch.Generator().manual_seed(1)) if reduction == "none" else None
+    nscale = None if scale is None else _np(scale)
+    s = np.abs(O.row_scale((y != IGN).numpy(), reduction, nscale))
+    kw = dict(reduction=reduction, grad_row_scale=None if scale is None else scale.cuda())
+    d = _cuda(X, W, y)
+    ws = torch.empty(F.policy_workspace_size(N, H, V, True), dtype=torch.uint8, device="cuda")
+    loss, *_ = F.policy_forward_backward(*d, *_cuda(old, adv), ref_logp=ref.cuda(), clip_high=0.28, kl_coef=0.05,
+                                         workspace=ws, **kw)
+    assert F.row_order_info(ws)[0]
+    want = O.policy_reference(Z, y, old, adv, ref, 0.2, 0.28, 0.05, reduction=reduction, grad_row_scale=nscale)[0]
+    # 1e-5 a row: the log-probabilities' error, times |dL/dlp| <= 1.28 |A| + kl |e^d - 1|
+    _close(loss.item(), want, (s * (1.3 * np.abs(_np(adv)) + 0.2)).sum() * 1e-5 + abs(want) * EPS32, "policy loss")
+    ws = torch.empty(F.distill_workspace_size(N, H, V, K, True), dtype=torch.uint8, device="cuda")
+    loss, *_ = F.distill_forward_backward(*d, *_cuda(ids, u), ce_weight=0.5, workspace=ws, **kw)
+    assert F.row_order_info(ws)[0]
+    want, _, rows = O.distill_reference(Z, y, ids, u, None, 1.0, 1.0, 0.5, reduction=reduction, grad_row_scale=nscale)
+    _close(loss.item(), want, (s * (1 + np.abs(rows))).sum() * 1e-5 + abs(want) * EPS32, "distillation loss")
+
+
+@pytest.mark.parametrize("N,H,V", [(700, 64, 60000), (3, 1024, 30000), (260, 520, 20011), (513, 136, 70001)])
+def test_distill_head_on_every_workspace(N, H, V):
+    """Wide chunks with and without the reordering area, and the least that a call
+    takes: the oracle's results, and the same bits again."""
+    F = _lib()
+    K = 12
+    X, W, Z, y, *_ = _head(N, H, V, seed=N, ign=0.0 if N < 5 else 0.55)
+    ids, u = teacher_case(N, V, K, seed=N)
+    d = _cuda(X, W, y, ids, u)
+    rloss, G, rrows = O.distill_reference(Z, y, ids, u, None, 1.0, 1.0, 0.5)
+    rX, rW = G @ _np(W), G.T @ _np(X)
+    for nbytes in (F.distill_workspace_size(N, H, V, K), F.distill_workspace_size(N, H, V, K, True),
+                   F.distill_workspace_size(N, H, 1, K)):
+        ws = torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+        loss, status, rows, dX, dW = F.distill_forward_backward(*d, ce_weight=0.5, row_loss=True, workspace=ws)
+        assert status.item() == 0
+        _close(_np(rows), rrows, 1e-4 * (1 + np.abs(rrows)), "row loss")
+        _close(loss.item(), rloss, 1e-5 * (1 + np.abs(rrows)).mean(), "loss")
+        assert_grad_close(_np(dX), rX, "dX")
+        assert_grad_close(_np(dW), rW, "dW")
+        again = F.distill_forward_backward(*d, ce_weight=0.5, row_loss=True, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(again, (loss, status, rows, dX, dW)))
+
+
+def test_another_stream_with_inputs_made_before_it():
+    """The side stream waits for the inputs once; every operator there has the bits
+    of the current stream's call."""
+    F = _lib()
+    Z, y, old, adv, ref = policy_case(64, 3001, seed=31, dtype=torch.bfloat16)
+    ids, u = teacher_case(64, 3001, 24, seed=31)
+    X, W, _, hy, hold, hadv, _ = _head(64, 64, 3001, seed=32)
+    Zd, yd, ld, od, ad, rd, idd, ud, Xd, Wd, hyd, hod, had = _cuda(Z, y, -old, old, adv, ref, ids, u, X, W, hy, hold, hadv)
+    calls = [lambda s=None: F.clipped_policy(ld, yd, rd, ad, stream=s),
+             lambda s=None: F.policy_loss(Zd, yd, od, ad, ref_logp=rd, kl_coef=0.1, entropy_coef=0.01, stream=s),
+             lambda s=None: F.distill_topk(Zd, yd, idd, ud, ce_weight=0.5, temperature=2.0, row_loss=True, stream=s),
+             lambda s=None: F.policy_forward_backward(Xd, Wd, hyd, hod, had, stream=s),
+             lambda s=None: F.distill_forward_backward(Xd, Wd, hyd, idd, ud, row_loss=True, stream=s)]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = [[call(side) for call in calls] for _ in range(5)]
+    torch.cuda.synchronize()
+    for outs in got:
+        for a, b in zip(want, outs):
+            assert all(torch.equal(x, z) for x, z in zip(a, b))
