@@ -315,12 +315,14 @@ flce_status_t flce_pairwise_logistic(const float* d_row_loss, const int32_t* y, 
  *
  * Rows whose target is ignore_index take part in nothing: whatever their
  * logits, log-probabilities, advantages or teacher entries hold (NaN
- * included), their outputs are 0.  So are those of a row whose target lies
- * outside [0, V), where V is given; it sets FLCE_ERR_TARGET_OUT_OF_RANGE in
- * d_status and still counts in n.  Reductions are those of
- * flce_forward_backward_ex: the loss is sum_i s_i L_i over the other rows with
- * s_i = 1/n, 1 or grad_row_scale[i].  A mean over each answer's tokens and
- * then over the answers is NONE with s_i = 1 / (answers * tokens of i's answer).
+ * included), their outputs are 0.  (Through the head, X has to be finite in
+ * every row: dW's product takes all of them, and 0 times NaN is NaN.)  So are
+ * those of a row whose target lies outside [0, V), where V is given; it sets
+ * FLCE_ERR_TARGET_OUT_OF_RANGE in d_status and still counts in n.  Reductions
+ * are those of flce_forward_backward_ex: the loss is sum_i s_i L_i over the
+ * other rows with s_i = 1/n, 1 or grad_row_scale[i].  A mean over each answer's
+ * tokens and then over the answers is NONE with s_i = 1 / (answers * tokens of
+ * i's answer).
  *
  * Logit tensors of these entries may be bf16, fp16 or fp32 (flce_dtype_t),
  * rows `ld` elements apart (ld >= V), elements of a row adjacent; pointers
@@ -402,7 +404,11 @@ flce_status_t flce_distill_topk(const void* logits, int32_t dtype, int64_t ld, c
  * workspace: flce_policy_workspace_size bytes (`reorder` != 0: with the area
  * that lets the call reorder token rows), which depends on V: small batches
  * take wider vocabulary chunks.  flce_workspace_size bytes are enough, at the
- * cross-entropy head's chunk width.  0 for invalid sizes. */
+ * cross-entropy head's chunk width.  0 for invalid sizes.
+ * One call at a time on a device, as of every entry that forms dX and dW: their
+ * pass 2 is a persistent kernel whose blocks wait for one another and count on
+ * all SMs; two at once may give up with FLCE_ERR_TIMEOUT.  Order calls on several
+ * streams by events. */
 size_t flce_policy_workspace_size(int64_t N, int64_t H, int64_t V, int32_t reorder);
 flce_status_t flce_policy_forward_backward(const uint16_t* X, const uint16_t* W, const int32_t* y, int64_t N,
                                            int64_t H, int64_t V, int32_t ignore_index, const float* d_old_logp,

@@ -26,10 +26,12 @@ constexpr int VC = 2048;
 // while G stays within 64 MB (half the L2): a chunk's first items wait for the
 // last ones of the chunk before, which is most of a small head's time, and the
 // running dX sum is read and written once per chunk.  Measured against 2048
-// (N x H x V): 256 x 256 x 4096 62 against 76 us, 16 x 4096 x 128256 1.45
-// against 3.17 ms, 512 x 4096 x 128256 2.07 against 3.30 ms, 2048 x 2304 x
-// 256000 6.7 against 7.5 ms.  G of 16 MB is 2 to 7% slower from 1024 rows on,
-// 128 MB the same as 64.
+// (policy head in a graph, N x H x V, with the dX ranges below that the wide layout
+// goes with): 256 x 256 x 4096 53 against 79 us, 16 x 4096 x 128256 1.03 against
+// 3.20 ms, 512 x 4096 x 128256 2.11 against 3.35 ms, 1024 x 2304 x 256000 4.5
+// against 5.4 ms, 2048 x 2304 x 256000 8.3 against 9.0 ms, where dX has one range.
+// G of 16 MB is 2 to 7% slower from 1024 rows on; 128 MB is 9% faster at 1024 x 2304
+// x 256000 and 3% slower at 8192 x 4096 x 128256.
 constexpr int64_t WIDE_G_BYTES = 64ll << 20;
 constexpr int64_t WIDE_CHUNK = 1 << 20;
 int wide_chunk(int64_t N, int64_t V) {
@@ -59,7 +61,7 @@ flce_status_t cuda_fail(int line) {
 // Ranges that the vocabulary of a chunk is split into for dX when the token and
 // hidden tiles alone are fewer than the SM pairs: as many as make one round of
 // items for the 74 pairs that a B200 has, each of 16 k-blocks at least.  Measured
-// against two rounds (N x H x V): 2048 x 2304 x 256000 7.88 against 8.90 ms, 1024 x
+// against two rounds (policy head, both on one GPU in turn, N x H x V): 2048 x 2304 x 256000 7.88 against 8.90 ms, 1024 x
 // 2304 x 256000 4.40 against 4.83 ms, 512 x 1024 x 50000 255 against 275 us, 16 x
 // 4096 x 128256 1.00 against 1.05 ms, 256 x 256 x 4096 the same.
 int dx_splits(int64_t N, int64_t H, int64_t V, int chunk) {
@@ -990,7 +992,7 @@ cudaError_t launch_logit_shape(const LogitArgs& a, int cs, int num_sms, int dev,
 // rows times what a row costs a warp, in tiles, the exchanges as one more.
 // Measured (bf16 policy loss, 256 threads / 128 / 32): 8192 x 32064 268 / 250 us,
 // 16384 x 4096 271 / 152 / 108 us, 16384 x 119 267 / 142 / 69 us; since then the
-// chosen ones have come down to 263, 81 and 45 us.
+// chosen ones have come down to 258, 82 and 45 us.
 int logit_threads(int64_t N, int64_t row_bytes, int cs, int num_sms) {
   if (cs > 1) return LOGIT_THREADS;
   const int64_t tiles = row_bytes / (TILE_CHUNKS * 16) + 1;

@@ -1700,7 +1700,9 @@ __global__ void __launch_bounds__(256)
 // Joins the vocabulary ranges' shares of dX (KS > 1): their sum in range order,
 // rounded once, in the caller's row order; rows of all-ignored tiles, which no
 // item computed, are zero.  A thread takes eight columns.  Bound by reading the
-// shares: three ranges of 2048 x 2304 (57 MB) 13 us, those of 256 x 256 4 to 5 us.
+// shares and by its launch: between events, where an empty kernel takes 6.5 us, two
+// ranges of 1024 x 2304 (19 MB) 12.7 us, nine of 512 x 1024 (19 MB) 10.7, those of
+// 256 x 256 6.7.
 __global__ void __launch_bounds__(256)
     flce_dx_join_kernel(const float* part, int KS, uint16_t* dX, const int* perm, const int* tile_valid, int N, int H) {
   const int h8 = H / 8;
@@ -1787,6 +1789,13 @@ constexpr int COMBINE_THREADS = 256;
 // Deterministic: a fixed tree inside each block, then the last block to finish
 // adds the block sums in block order, in fp64.  (The target range was checked
 // by the row-order kernel.)
+// A row's log-sum-exp is fp32, good to 2^-24 of its log2 and the merge's few
+// roundings, about 1e-6: as the cross-entropy head has it, so that the policy
+// head's log-probabilities are its row losses with the sign turned, bit for bit.
+// What the policy step computes in fp64 from such an lp has no more digits than lp;
+// fp64 is there for the clip borders and the KL term's small difference, on which
+// flce_clipped_policy, given the same lp, has to agree.  A distillation call merges
+// its splits in fp64, because its loss is a small difference of large terms.
 // A vocabulary shard's call (COMBINE_SHARD) stops after writing its rows'
 // (lse, target logit); the call after the exchange (COMBINE_SHARDS_IN) takes
 // lse_i as the log-sum-exp of every shard's lse and z_{i,y_i} as the sum of

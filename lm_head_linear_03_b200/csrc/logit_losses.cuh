@@ -134,7 +134,8 @@ __device__ __forceinline__ float load_as_f32(const void* p, int dtype, size_t i)
 // (count_rows), so nothing has to be zeroed ahead.  It costs its launch: in a
 // graph a clipped-policy call takes 8.2 us at 4096 rows with it and 4.2 us at 512
 // without.  Counting in every CTA of the next launch instead would read the
-// targets once per CTA, and the ticket would need a memset, a node of its own.
+// targets once per CTA, which a few rows could bear; the ticket would still have to
+// be zero before that launch.  Not built, nor a launch that overlaps the next.
 constexpr int BEGIN_THREADS = 512;
 constexpr int BEGIN_ROWS = 16 * BEGIN_THREADS;  // per block; more when that would take over BEGIN_BLOCKS blocks
 constexpr int BEGIN_BLOCKS = 256;
@@ -246,9 +247,12 @@ struct PolicyRowsArgs {
 // Elementwise over the rows, with two fp64 exponentials (the ratio, the KL term) in
 // each.  A thread takes four neighbouring rows, so that the loads of each of its up
 // to six streams are one 16-byte access where the stream allows it.  Measured, both
-// launches in a graph: 1,048,576 rows (34 MB) 16.4 us, 4,194,304 rows 43 us, 3.1 TB/s.
-// Instructions of the fp64 functions bound it (52% of the issue slots, the fp64
-// pipe 23%); fewer registers for 5, 6 or 8 CTAs on an SM: 44.0, 45.3, 46.5 us.
+// launches in a graph: 1,048,576 rows (34 MB) 16.7 us, 4,194,304 rows 43 to 47 us,
+// 3.1 to 2.8 TB/s.
+// No unit is full (52% of the issue slots, the fp64 pipe 23%): what bounds it is
+// latency, of the loads and of the exponentials' chains, which run one after the
+// other because each of a thread's rows lies behind a branch.  Fewer registers for
+// 5, 6 or 8 CTAs on an SM: 44.0, 45.3, 46.5 us against 43.0.
 constexpr int POLICY_THREADS = 256;
 constexpr int POLICY_ROWS = 4;
 
@@ -460,9 +464,10 @@ __device__ __forceinline__ bool row_counts(const LogitArgs& a, int y) {
 
 // Persistent CTAs, each with a row (or, in clusters, its part of a row) at a
 // time.  A row is walked twice: forwards for its maximum and sums, backwards
-// for the gradient.  The second read finds the row in L2, where the first one's
-// policy keeps it: the rows under way on all SMs are some 80 MB at most (the
-// host gives longer rows to clusters).  Memory is thus read and written once,
+// for the gradient.  The second read finds most of the row in L2, where the first
+// one's policy keeps it: the rows under way on all SMs are some 80 MB at most, as
+// the host gives rows of over 256 KB to clusters; from 2 MB on, the largest
+// cluster's parts grow again.  Memory is thus read and written about once,
 // and what a row costs beside its elements (two exchanges, the fp64 of its
 // scalars) is paid once per 100,000 elements or so.
 //
@@ -480,14 +485,15 @@ __device__ __forceinline__ bool row_counts(const LogitArgs& a, int y) {
 //
 // Two exponentials per element, one per walk: probabilities kept from the first
 // walk would be a second array to write and read.  Measured in a graph, with the
-// first launch: policy loss, bf16 4096 x 128256 427 us (2.10 GB, 4.9 TB/s), with a
-// quarter of the rows ignored (not read) 398 us; distillation, bf16 2048 x 256000,
-// 64 entries 470 us and 431 us; fp16 1023 x 50021 with unaligned rows 59 us.  On
-// 1184 x 128256 alone 131 us: 4.7 TB/s from and to DRAM, 57% of the issue slots,
-// 56% of the exponential unit.  No unit is full; with 16 warps on an SM (128
-// registers each, for eight chunks of a tile in flight) what remains is latency.
-// Three CTAs on an SM (80 registers), tiles of 2 KB, a gradient stored from
-// registers and refills in another order measured the same or slower.
+// first launch: policy loss, bf16 4096 x 128256 427 us (2.10 GB, 4.9 TB/s), with an
+// entropy term 447 us, with a quarter of the rows ignored (not read) 408 us;
+// distillation, bf16 2048 x 256000, 64 entries 470 us and 432 us; fp16 1023 x
+// 50021, a fifth ignored, 60 us.  On 1184 x 128256 alone, with an entropy term, 133
+// us: 4.6 TB/s from and to DRAM, 58% of the issue slots, 56% of the exponential
+// unit.  No unit is full; with 16 warps on an SM (128 registers each, for eight
+// chunks of a tile in flight) what remains is latency.  Three CTAs on an SM (80
+// registers), tiles of 2 KB, a gradient stored from registers and refills in
+// another order measured the same or slower.
 template <typename T, int LOSS, int THREADS>
 __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_logit_loss_kernel(const LogitArgs a) {
   using L = LogitTraits<T>;
@@ -799,7 +805,9 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
       const double inv_l = 1.0 / sum_l;
       double lnL = log(sum_l);
       const double mean = sum_t * inv_l;  // policy: E[z - m]
-      // zs is off by zs_off of itself: d ln L / d ln zs = E[z - m] / T
+      // zs is off by zs_off of itself: d ln L / d ln zs = E[z - m] / T.  Distillation has
+      // no such mean; it keeps an error of 2^-25 of it, some 1e-6 where the row's
+      // logits lie tens of T below their maximum.
       if (is_policy(LOSS)) lnL -= a.zs_off * a.inv_T * mean;
       const float zy = L::load(&zy_raw);
       double total = 0.0;
@@ -875,8 +883,8 @@ __global__ void __launch_bounds__(THREADS, 2 * LOGIT_THREADS / THREADS) flce_log
         f32x2_split(mul2(d0, zs2), lo, hi);
         const uint64_t e = f32x2(ex2_approx(lo), ex2_approx(hi));
         // b (z - m) may overflow where e is 0, with a logit near the largest fp32 value:
-        // e (z - m) comes first.  4096 x 128256 takes 1% longer than with e (a + b (z - m)),
-        // as with a choice between the two per row.  fp16 has no such logits.
+        // e (z - m) comes first.  4096 x 128256 takes 444 -> 452 us for it, and 1% longer
+        // than before with a choice between the two per row.  fp16 has no such logits.
         if constexpr (LOSS == LOSS_POLICY_ENT && L::CLAMPS) return fma2(mul2(e, d0), b2, mul2(e, a2));
         if constexpr (LOSS == LOSS_POLICY_ENT) return mul2(e, fma2(b2, d0, a2));
         if constexpr (LOSS == LOSS_DISTILL2) {

@@ -10,7 +10,8 @@ device tensors without waiting, the device status word (0, or a
 ``flce_status_t``) among them.
 
 ``stream``: the CUDA stream to run on (default: the current one).  The call does
-not make ``stream`` wait for the streams that produced its inputs.
+not make ``stream`` wait for the streams that produced its inputs.  Calls through
+the head run one at a time on a device: order those on several streams by events.
 """
 from __future__ import annotations
 
